@@ -31,6 +31,8 @@
 #ifndef FAVOR_H
 #define FAVOR_H
 
+#include <stddef.h>
+
 #if defined(__GNUC__)
 #define FAVOR_API __attribute__((visibility("default")))
 #else
@@ -324,6 +326,153 @@ FAVOR_API favor_status favor_attn_bidir_noalloc(const float* omega, int H, int m
 /* favor_destroy -- free everything the handle owns (after synchronising its
  * device).  Accepts NULL. */
 FAVOR_API favor_status favor_destroy(favor_handle h);
+
+/*
+ * Selective state space scan with its short causal convolution, for prompts,
+ * single tokens and training: the other linear-time token mixer beside FAVOR+
+ * attention, a state per channel decayed by a rate that the token itself sets.
+ * With D channels, N states a channel, G groups of B and C, K filter taps:
+ *
+ *   convolution  p[t,c] = bias[c] + sum_k w[c,k] x[t-K+1+k, c],
+ *                out = p, or p / (1 + e^-p) with silu != 0
+ *   scan         dt = log(1 + e^(raw + dt_bias)),
+ *                h_n[t] = e^(dt A_n) h_n[t-1] + dt u B_n,
+ *                y = sum_n C_n h_n[t] + skip u,
+ *                out = y, or y z / (1 + e^-z) where z is given
+ *   for every channel c; group g = c / (D / G) names its B and C.
+ *
+ * Tensors are contiguous, token-major and of the handle's dtype, as a
+ * projection writes them:
+ *   x, u, dt (the raw step), z, out, dout: [B, L, D]    Bm, Cm: [B, L, G, N]
+ * Parameters are DEVICE float arrays whatever the dtype:
+ *   weight [D, K], bias [D], A [D, N] (decay rates, in general negative),
+ *   skip [D], dt_bias [D].  bias, skip, z and dt_bias may be NULL (absent).
+ * Arithmetic, states and sums are fp32; outputs are rounded once.
+ *
+ * States.  A scan state is a page [D, N] of float, a convolution window a page
+ * [K-1, D] of the dtype (the last K-1 inputs, oldest first); a pool holds
+ * n_pages of them, a scan pool 16-byte aligned.  A zero page is an empty past.
+ * `pages` is a DEVICE int array [B], the page of each row, or NULL: row b uses
+ * page b (n_pages >= B).  A row whose page is outside [0, n_pages) takes no
+ * part (padding of a batch of fixed size); where several rows name one page,
+ * the first has it and the others take no part.  A row that takes no part gets
+ * zeros in out.  The others read their page, and leave in it the state behind
+ * their last token.
+ * `lens` is a DEVICE int array [B] or NULL: row b has lens[b] tokens (clamped
+ * to [0, L]); rows of out, and of the gradients dx, du, ddt, dz, dB and dC,
+ * behind a row's end are neither read nor written.
+ *
+ * Same rules as for a favor_handle: every call only enqueues work on `stream`,
+ * checks run on the host before any launch, a handle belongs to the device that
+ * was current at its creation.  favor_ssm_scan and the backward calls use the
+ * handle's workspace, so those calls on one handle (a graph's replays among
+ * them) must not overlap in time on the device; favor_conv_causal and the step
+ * calls use none and may overlap anything that does not share their tensors.
+ * Outputs and pools must not overlap any other argument (INVALID_ARG).
+ */
+typedef struct favor_ssm_s* favor_ssm;
+
+/*
+ * favor_ssm_create -- a handle for D channels, N states, G groups, K taps.
+ * Supported: N in {8, 16, 32, 64}, K in {2, 3, 4} (else FAVOR_ERR_UNSUPPORTED);
+ * D a multiple of G, of any size up to 2^20; max_B*max_L up to 2^30 and
+ * max_B*max_L*D up to 2^36.  training != 0 allocates the backward calls'
+ * workspace (8*N*G bytes a token for every 512 / N channels of a group, and
+ * 12*N*D bytes for every 128 tokens of a row); without it they give
+ * FAVOR_ERR_UNSUPPORTED.
+ */
+FAVOR_API favor_status favor_ssm_create(favor_ssm* out, int D, int N, int G, int K, favor_dtype dtype, int max_B,
+                                        int max_L, int training);
+/* favor_ssm_destroy -- free everything the handle owns (after synchronising its
+ * device).  Accepts NULL. */
+FAVOR_API favor_status favor_ssm_destroy(favor_ssm h);
+
+/*
+ * favor_conv_causal -- the convolution of a prompt, or of the next L tokens of
+ * sequences whose past is in their window pages.  window NULL: empty past, and
+ * nothing is kept.  favor_conv_causal_step: one token a row, x and out [B, D];
+ * window is required.
+ */
+FAVOR_API favor_status favor_conv_causal(favor_ssm h, const void* x, const float* weight, const float* bias, int silu,
+                                         void* window, const int* pages, int n_pages, const int* lens, void* out,
+                                         int B, int L, void* stream);
+FAVOR_API favor_status favor_conv_causal_step(favor_ssm h, const void* x, const float* weight, const float* bias,
+                                              int silu, void* window, const int* pages, int n_pages, void* out,
+                                              int B, void* stream);
+
+/*
+ * favor_conv_causal_backward -- gradients of favor_conv_causal with an empty
+ * past: dx [B, L, D] of the dtype, dweight [D, K] and dbias [D] (may be NULL)
+ * float, all written, not added to.  Fixed-order sums (bitwise repeatable).
+ */
+FAVOR_API favor_status favor_conv_causal_backward(favor_ssm h, const void* x, const float* weight, const float* bias,
+                                                  int silu, const int* lens, const void* dout, void* dx,
+                                                  float* dweight, float* dbias, int B, int L, void* stream);
+
+/*
+ * favor_ssm_scan -- the scan of a prompt, or of the next L tokens of sequences
+ * whose state is in their pages.  state NULL: empty past, and nothing is kept.
+ * favor_ssm_scan_step: one token a row (u, dt, z, out [B, D], Bm, Cm
+ * [B, G, N]); state is required.
+ */
+FAVOR_API favor_status favor_ssm_scan(favor_ssm h, const void* u, const void* dt, const float* A, const void* Bm,
+                                      const void* Cm, const float* skip, const void* z, const float* dt_bias,
+                                      float* state, const int* pages, int n_pages, const int* lens, void* out, int B,
+                                      int L, void* stream);
+FAVOR_API favor_status favor_ssm_scan_step(favor_ssm h, const void* u, const void* dt, const float* A, const void* Bm,
+                                           const void* Cm, const float* skip, const void* z, const float* dt_bias,
+                                           float* state, const int* pages, int n_pages, void* out, int B,
+                                           void* stream);
+
+/*
+ * favor_ssm_scan_backward -- gradients of favor_ssm_scan with an empty past for
+ * the upstream gradient dout; the forward's states are formed again.  du, ddt
+ * (of the raw step), dz, dB, dC in the dtype; dA [D, N], dskip, ddt_bias [D]
+ * float; all written, not added to.  dskip, dz and ddt_bias are given exactly
+ * where skip, z and dt_bias are (INVALID_ARG).  Fixed-order sums.
+ */
+FAVOR_API favor_status favor_ssm_scan_backward(favor_ssm h, const void* u, const void* dt, const float* A,
+                                               const void* Bm, const void* Cm, const float* skip, const void* z,
+                                               const float* dt_bias, const int* lens, const void* dout, void* du,
+                                               void* ddt, float* dA, void* dB, void* dC, float* dskip, void* dz,
+                                               float* ddt_bias, int B, int L, void* stream);
+
+/*
+ * Pages of a cache of states: a pool is n_pages blocks of page_bytes bytes, of
+ * whatever kind (scan states, convolution windows, the [H, m, dv+1] states of
+ * the stateful FAVOR+ calls).  Index arrays are DEVICE int arrays.  No handle,
+ * no workspace; only enqueued on `stream`, on the current device.
+ *
+ * favor_pages_copy -- page dst[i] of dst_pool becomes a copy of page src[i] of
+ * src_pool, for n pairs; a source named several times is forked.  The pools may
+ * be the same one (else they must not overlap).  A pair is left out if a page is
+ * outside its pool, if an earlier pair names its destination, or if the pools
+ * are the same and any pair of the call reads its destination (a pair with
+ * src = dst in one pool has nothing to do and counts as done unless another
+ * rule leaves it out): so the result does not depend on the order of copies.
+ * done [n], or NULL: 1 for a pair carried out, 0 for one left out.
+ *
+ * favor_pages_clear -- the n pages named become zero, the empty state; entries
+ * outside the pool are passed over.
+ *
+ * favor_pages_compact -- table [S] names the live pages (an entry outside
+ * [0, n_pages) names none; a page may be named several times).  With U live
+ * pages, those at U or above move, in order, into the free pages below U, and
+ * new_table [S] names where each entry's page is now (-1 where it names none).
+ * n_live [1] is U.  page_map [n_pages], or NULL, is where each page went (-1 for
+ * a free one).  Pages at U and above hold what they held.  n_pages <= 131072.
+ *
+ * favor_pages_move -- moves the pages of another pool by the page_map of a
+ * compaction (pools of one cache share the table).
+ */
+FAVOR_API favor_status favor_pages_copy(void* dst_pool, int n_dst, const void* src_pool, int n_src, size_t page_bytes,
+                                        const int* src, const int* dst, int n, int* done, void* stream);
+FAVOR_API favor_status favor_pages_clear(void* pool, int n_pages, size_t page_bytes, const int* pages, int n,
+                                         void* stream);
+FAVOR_API favor_status favor_pages_compact(void* pool, int n_pages, size_t page_bytes, const int* table, int S,
+                                           int* new_table, int* page_map, int* n_live, void* stream);
+FAVOR_API favor_status favor_pages_move(void* pool, int n_pages, size_t page_bytes, const int* page_map,
+                                        void* stream);
 
 /* Name of a status code (static string). */
 FAVOR_API const char* favor_status_str(favor_status s);

@@ -44,7 +44,11 @@ EXPORTED_SYMBOLS = ("favor_create", "favor_feature_map", "favor_attn_bidir", "fa
                     "favor_kv_state", "favor_attn_from_state", "favor_attn_causal_step",
                     "favor_attn_bidir_backward", "favor_attn_causal_backward",
                     "favor_attn_causal_gated", "favor_attn_causal_step_gated", "favor_set_relpos",
-                    "favor_check_bounded_wait")
+                    "favor_check_bounded_wait",
+                    "favor_ssm_create", "favor_ssm_destroy", "favor_conv_causal", "favor_conv_causal_step",
+                    "favor_conv_causal_backward", "favor_ssm_scan", "favor_ssm_scan_step",
+                    "favor_ssm_scan_backward", "favor_pages_copy", "favor_pages_clear", "favor_pages_compact",
+                    "favor_pages_move")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -115,6 +119,8 @@ def lib() -> ctypes.CDLL:
                    "favor_attn_bidir_backward", "favor_attn_causal_backward", "favor_attn_causal_gated",
                    "favor_attn_causal_step_gated", "favor_set_relpos"):
             getattr(L, fn).restype = ctypes.c_int
+        from . import ssm
+        ssm.declare(L)
         _LIB = L
     return _LIB
 

@@ -1,0 +1,133 @@
+"""GPU tests of the page calls: copies and forks, clearing, compaction, against the oracle's rules;
+results are copies of bytes, so they are equal."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import random_feature_gb300 as R
+
+pytestmark = pytest.mark.gpu
+
+# page shapes and types: 16-byte, 4-byte, 2-byte and 1-byte multiples, pages longer than a block's share
+PAGES = [((4, 64), torch.float32), ((5,), torch.float32), ((3, 7), torch.bfloat16), ((13,), torch.uint8),
+         ((257, 65), torch.float32), ((3, 1001), torch.bfloat16)]
+
+
+def _pool(P, page, dtype, seed):
+    r = np.random.default_rng(seed)
+    return torch.from_numpy(r.integers(0, 120, (P, *page)).astype(np.uint8)).to("cuda", dtype)
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _np(t):
+    return t.float().cpu().numpy()
+
+
+@pytest.mark.parametrize("page,dtype", PAGES, ids=[f"{'x'.join(map(str, p))}-{str(d)[6:]}" for p, d in PAGES])
+def test_copy_and_fork(page, dtype):
+    a, b = _pool(9, page, dtype, 1), _pool(6, page, dtype, 2)
+    src, dst = [1, 1, 8, 9, -1, 0, 3, 2 ** 31 - 1], [0, 3, 3, 1, 2, 6, 5, 4]
+    want, done = O.pages_copy(_np(b), _np(a), src, dst, same=False)
+    got = R.pages_copy(b, a, _ints(src), _ints(dst))
+    assert got.tolist() == done == [1, 1, 0, 0, 0, 0, 1, 0]
+    assert np.array_equal(_np(b), want)
+    # one pool: forks, a destination that the call reads, one named twice, a page onto itself
+    src, dst = [1, 1, 4, 5, 7, 2], [0, 3, 5, 6, 7, 0]
+    want, done = O.pages_copy(_np(a), _np(a), src, dst, same=True)
+    got = R.pages_copy(a, a, _ints(src), _ints(dst))
+    assert got.tolist() == done == [1, 1, 0, 1, 1, 0]
+    assert np.array_equal(_np(a), want)
+
+
+@pytest.mark.parametrize("page,dtype", PAGES, ids=[f"{'x'.join(map(str, p))}-{str(d)[6:]}" for p, d in PAGES])
+def test_clear(page, dtype):
+    a = _pool(7, page, dtype, 3) + 1
+    want = _np(a)
+    want[[2, 6]] = 0
+    R.pages_clear(a, _ints([6, -1, 2, 7, 2]))
+    assert np.array_equal(_np(a), want)
+
+
+@pytest.mark.parametrize("P,S,seed", [(1, 1, 0), (5, 3, 1), (40, 25, 2), (64, 64, 3), (1000, 300, 4), (3001, 2000, 5)])
+def test_compact(P, S, seed):
+    r = np.random.default_rng(seed)
+    table = r.integers(-2, P + 2, S).tolist()
+    pool, win = _pool(P, (3, 8), torch.float32, seed), _pool(P, (5,), torch.bfloat16, seed + 1)
+    want, new, live, where = O.pages_compact(_np(pool), table)
+    wwin = O.pages_compact(_np(win), table)[0]
+    got, n = R.pages_compact(pool, _ints(table), others=[win])
+    assert got.tolist() == new and n.tolist() == [live]
+    assert np.array_equal(_np(pool), want) and np.array_equal(_np(win), wwin)
+    # again: nothing is left to move
+    again, n = R.pages_compact(pool, got, others=[win])
+    assert torch.equal(again, got) and n.tolist() == [live] and np.array_equal(_np(pool), want)
+
+
+@pytest.mark.parametrize("table", [[-1, -1], [9, 3], [0, 1, 2], [11] * 5, list(range(11, -1, -1)), [6, 7, 8, 9, 10, 11]])
+def test_compact_extremes(table):
+    pool = _pool(12, (300,), torch.float32, 6)
+    want, new, live, _ = O.pages_compact(_np(pool), table)
+    got, n = R.pages_compact(pool, _ints(table))
+    assert got.tolist() == new and n.tolist() == [live] and np.array_equal(_np(pool), want)
+
+
+def test_compact_largest_table():
+    """As many pages as the call takes."""
+    P = 1 << 17
+    r = np.random.default_rng(7)
+    table = r.integers(0, P, 50000)
+    pool = torch.arange(P, device="cuda", dtype=torch.int32)[:, None].contiguous()
+    got, n = R.pages_compact(pool, _ints(table.tolist()))
+    uniq = np.unique(table)
+    U = len(uniq)
+    assert n.item() == U
+    # every entry's page holds what it held, pages below U are the live ones, those already there stayed
+    now = got.cpu().numpy()
+    host = pool.cpu().numpy()[:, 0]
+    assert np.array_equal(host[now], table) and now.max() < U and np.array_equal(np.sort(host[:U]), uniq)
+    assert np.array_equal(now[table < U], table[table < U])
+    low = np.setdiff1d(np.arange(U), uniq)
+    assert np.array_equal(host[low], uniq[uniq >= U])
+
+
+def test_pages_of_a_serving_cache():
+    """Favor states and scan states of a few sequences in pages: decode, fork a beam, free a sequence,
+    compact, decode on; every sequence goes on as it does alone."""
+    D, N, P = 48, 16, 10
+    r = np.random.default_rng(8)
+    f32 = lambda *s: torch.from_numpy(r.standard_normal(s).astype(np.float32)).cuda()
+    A = -torch.exp(f32(D, N))
+    w = f32(D, 4)
+    with R.Ssm(D, N, 1, 4, "f32", P, 8, training=False) as f:
+        def step(x, dt, Bm, Cm, win, state, pages=None):
+            return f.scan_step(f.conv_step(x, w, win, pages=pages), dt, A, Bm, Cm, state, pages=pages)
+        tok = lambda n: (f32(n, D), f32(n, D), f32(n, 1, N), f32(n, 1, N))
+        win, state = f.new_window(P), f.new_state(P)
+        slots = [7, 2, 9]
+        alone = [(f.new_window(1), f.new_state(1)) for _ in slots]
+        def both(slots, alone):
+            t = tok(len(slots))
+            got = step(*t, win, state, _ints(slots))
+            want = torch.cat([step(*(a[i:i + 1] for a in t), *alone[i]) for i in range(len(slots))])
+            assert torch.equal(got, want)
+        for _ in range(3):
+            both(slots, alone)
+        # sequence 0 forks into page 4; sequence 1 is freed
+        assert R.pages_copy(state, state, _ints([7]), _ints([4])).item() == 1
+        assert R.pages_copy(win, win, _ints([7]), _ints([4])).item() == 1
+        slots, alone = [7, 9, 4], [alone[0], alone[2], tuple(t.clone() for t in alone[0])]
+        both(slots, alone)
+        table, n = R.pages_compact(state, _ints(slots), others=[win])
+        assert n.item() == 3 and sorted(table.tolist()) == [0, 1, 2]
+        slots = table.tolist()
+        for _ in range(2):
+            both(slots, alone)
+        # a new sequence on a page that held another one
+        new = next(p for p in range(P) if p not in slots)
+        R.pages_clear(state, _ints([new]))
+        R.pages_clear(win, _ints([new]))
+        both(slots + [new], alone + [(f.new_window(1), f.new_state(1))])

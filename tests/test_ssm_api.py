@@ -1,0 +1,114 @@
+"""Refusals of the scan, convolution and page calls that need no GPU: every argument check runs on
+the host before anything is launched."""
+import ctypes
+
+import pytest
+
+import random_feature_gb300 as R
+from random_feature_gb300 import build as _build
+
+BAD, UNS = R.FAVOR_ERR_INVALID_ARG, R.FAVOR_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built_library():
+    _build.build()
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(D=0), BAD), (dict(N=0), BAD), (dict(G=0), BAD), (dict(K=0), BAD), (dict(max_B=0), BAD), (dict(max_L=0), BAD),
+    (dict(dtype=2), BAD), (dict(G=3), BAD), (dict(N=12), UNS), (dict(N=128), UNS), (dict(K=1), UNS), (dict(K=5), UNS),
+    (dict(D=1 << 21), UNS), (dict(max_B=1 << 16, max_L=1 << 15), UNS), (dict(D=1 << 20, max_L=1 << 20), UNS),
+])
+def test_create_refuses(kw, want):
+    a = {**dict(D=64, N=16, G=1, K=4, dtype=0, max_B=2, max_L=128), **kw}
+    h = ctypes.c_void_p(12345)
+    n0 = R.favor_launch_count()
+    st = R.lib().favor_ssm_create(ctypes.byref(h), a["D"], a["N"], a["G"], a["K"], a["dtype"], a["max_B"], a["max_L"], 1)
+    assert st == want, R.favor_last_error()
+    assert h.value is None and R.favor_last_error() and R.favor_launch_count() == n0
+
+
+def test_null_handles():
+    L = R.lib()
+    assert L.favor_ssm_create(None, 64, 16, 1, 4, 0, 1, 1, 1) == BAD
+    assert L.favor_conv_causal(None, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, None) == BAD
+    assert L.favor_conv_causal_step(None, 1, 1, 1, 1, 1, 1, 1, 1, 1, None) == BAD
+    assert L.favor_conv_causal_backward(None, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, None) == BAD
+    assert L.favor_ssm_scan(None, *[1] * 15, None) == BAD
+    assert L.favor_ssm_scan_step(None, *[1] * 13, None) == BAD
+    assert L.favor_ssm_scan_backward(None, *[1] * 20, None) == BAD
+    assert L.favor_ssm_destroy(None) == R.FAVOR_OK
+
+
+MB = 1 << 20
+
+
+@pytest.mark.parametrize("call,want", [
+    (lambda L: L.favor_pages_copy(None, 4, MB, 4, 16, 1, 1, 1, None, None), BAD),
+    (lambda L: L.favor_pages_copy(MB, 0, MB, 4, 16, 4, 4, 1, None, None), BAD),
+    (lambda L: L.favor_pages_copy(MB, 4, 2 * MB, 4, 0, 4, 4, 1, None, None), BAD),
+    (lambda L: L.favor_pages_copy(MB, 4, 2 * MB, 4, 16, None, 4, 1, None, None), BAD),
+    (lambda L: L.favor_pages_copy(MB, 4, 2 * MB, 4, 16, 4, 4, 0, None, None), BAD),
+    (lambda L: L.favor_pages_copy(MB, 4, MB + 32, 4, 16, 4, 4, 1, None, None), BAD),      # pools overlap in part
+    (lambda L: L.favor_pages_copy(MB, 1 << 30, 2 * MB, 4, 1 << 20, 4, 4, 1, None, None), UNS),
+    (lambda L: L.favor_pages_clear(None, 4, 16, 4, 1, None), BAD),
+    (lambda L: L.favor_pages_clear(MB, 4, 16, None, 1, None), BAD),
+    (lambda L: L.favor_pages_clear(MB, 4, 16, 4, 0, None), BAD),
+    (lambda L: L.favor_pages_compact(None, 4, 16, 4, 1, 64, None, 128, None), BAD),
+    (lambda L: L.favor_pages_compact(MB, 4, 16, None, 1, 64, None, 128, None), BAD),
+    (lambda L: L.favor_pages_compact(MB, 4, 16, 4, 0, 64, None, 128, None), BAD),
+    (lambda L: L.favor_pages_compact(MB, 4, 16, 64, 3, 72, None, 128, None), BAD),        # table and new_table overlap
+    (lambda L: L.favor_pages_compact(MB, 4, 16, 64, 3, 96, 100, 128, None), BAD),         # new_table and page_map
+    (lambda L: L.favor_pages_compact(MB, (1 << 17) + 1, 16, 4, 1, 64, None, 128, None), UNS),
+    (lambda L: L.favor_pages_move(None, 4, 16, 4, None), BAD),
+    (lambda L: L.favor_pages_move(MB, 4, 16, None, None), BAD),
+])
+def test_page_calls_refuse(call, want):
+    n0 = R.favor_launch_count()
+    assert call(R.lib()) == want, R.favor_last_error()
+    assert R.favor_last_error() and R.favor_launch_count() == n0
+
+
+@pytest.mark.gpu
+def test_calls_refuse():
+    """Bad calls on a good handle: refused before any launch, the tensors untouched."""
+    import torch
+    D, N, B, L = 32, 16, 2, 12
+    t = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")
+    f4 = torch.float32
+    u, bc, A, w = t(B, L, D), t(B, L, 1, N), t(D, N, dtype=f4), t(D, 4, dtype=f4)
+    with R.Ssm(D, N, 1, 4, "bf16", B, L, training=False) as f:
+        st, win = f.new_state(B), f.new_window(B)
+        n0 = R.favor_launch_count()
+        for bad in (lambda: f.scan(u.float(), u, A, bc, bc), lambda: f.scan(u, u[:, :5], A, bc, bc),
+                    lambda: f.scan(u, u, A.bfloat16(), bc, bc), lambda: f.scan(u, u, A, bc[..., :8], bc),
+                    lambda: f.scan(u, u, A, bc, bc, state=st.bfloat16()), lambda: f.scan(u, u, A.cpu(), bc, bc),
+                    lambda: f.scan(u, u, A, bc, bc, lens=torch.zeros(B, device="cuda")),
+                    lambda: f.scan(u, u, A, bc, bc, state=st, pages=torch.zeros(B + 1, dtype=torch.int32, device="cuda")),
+                    lambda: f.scan(u.transpose(1, 2), u, A, bc, bc), lambda: f.scan(u[0], u, A, bc, bc),
+                    lambda: f.conv(u, w[:, :3]), lambda: f.conv(u, w, window=win[:, :2]),
+                    lambda: f.conv_step(u, w, win), lambda: f.conv(u, w, out=torch.empty_like(u)[:, :3]),
+                    lambda: R.pages_copy(st, win, t(1, dtype=torch.int32), t(1, dtype=torch.int32)),
+                    lambda: R.pages_copy(st, st, t(1, dtype=torch.int32), t(2, dtype=torch.int32)),
+                    lambda: R.pages_clear(st, t(1, dtype=torch.int64)), lambda: R.pages_clear(st[:, ::2], t(1, dtype=torch.int32)),
+                    lambda: R.pages_compact(st, t(0, dtype=torch.int32)),
+                    lambda: R.pages_compact(st, t(1, dtype=torch.int32), others=[win[:1]])):
+            with pytest.raises(ValueError):
+                bad()
+        one = f.new_state(1)
+        for bad, status in ((lambda: f.scan(u, u, A, bc, bc, out=u), BAD),                      # out over an input
+                            (lambda: f.conv(u, w, out=u), BAD),
+                            (lambda: f.scan(u, u, A, bc, bc, state=one), BAD),                  # too few pages
+                            (lambda: f.scan(u, u, A, bc, bc, pages=t(B, dtype=torch.int32)), BAD),   # pages, no state
+                            (lambda: f.scan(t(B + 1, L, D), t(B + 1, L, D), A, t(B + 1, L, 1, N), t(B + 1, L, 1, N)), BAD),
+                            (lambda: f.conv(t(B, L + 1, D), w), BAD),
+                            (lambda: f.scan_backward(u, u, A, bc, bc, u), UNS),                 # no training workspace
+                            (lambda: f.conv_backward(u, w, u), UNS)):
+            with pytest.raises(R.FavorError) as e:
+                bad()
+            assert e.value.status == status, str(e.value)
+        with pytest.raises(R.FavorError) as e:      # the state's pages are read 16 bytes at a time
+            R.favor_ssm_scan(f.handle, u, u, A, bc, bc, None, None, None, st.data_ptr() + 4, None, B, None,
+                             torch.empty_like(u), B, L)
+        assert e.value.status == BAD and R.favor_launch_count() == n0
