@@ -4,41 +4,31 @@
 //     y = sum_n C_n h_n + skip u,    out = y silu(z)
 // u, raw, z, out are [B, L, D]; B and C [B, L, G, N], group g serving the channels
 // g D/G .. (g+1) D/G - 1.  States and every sum are fp32.
+#include <type_traits>
+
 #include "ssm_internal.h"
 
 namespace favor {
 
 constexpr int kScanThreads = 128;
 
-// Two floats in one 64-bit register pair: the packed FMA / MUL issue two states'
-// arithmetic in one slot.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
-    float lo, hi;
-    unpack2(v, lo, hi);
-    return pack2(ex2_approx(lo), ex2_approx(hi));
-}
-
 // How a launch cuts channels and tokens.  A block is 128 threads over CPB
-// channels of one group of one row, LPC = N / NS lanes a channel (NS states in
-// each lane's registers), for one chunk of tokens, walked in tiles of 8 LPC.
+// channels of one group of one row, for one chunk of tokens walked in tiles of
+// TT.  A thread holds 8 states of 2 channels, LPC = N / 8 lanes a channel pair.
+//
+// What bounds it: at N = 16 a token of 32 channels (one warp's) takes 64 packed
+// FMAs and MULs' worth of register reads.  On this device an instruction reads
+// two 32-bit operand words a clock: fma.f32x2 of three distinct operands issues
+// every 3.1 clocks, of two every 2.2, mul.f32x2 every 2.1 (a plain fma: 1.5), so
+// the 32 of a token take 85 clocks of a quarter SM, beside 80 of exponentials
+// (ex2: one in 4) and 115 issue slots.  Measured with full waves: 150 clocks, 4.1
+// ns a thousand (token, channel) pairs; taking out the exponentials, or the
+// loads of B and C, changes that by 1 and 4%.  Two channels a thread share the
+// B and C that every lane loads (one channel a thread: 344 us against 328 at
+// [16, 512, 8192]); a next token's decays formed between this one's updates:
+// 342 us; 5 blocks an SM in 102 registers: 342 us.
+constexpr int kScanNS = 8, kScanCH = 2, kScanPerSm = 4;
+
 struct ScanPlan {
     int tiles;     // channel tiles a row (over all groups)
     int tpg;       // channel tiles a group
@@ -56,15 +46,45 @@ struct ScanWs {
 
 // SUMMARY: the first pass of a call with several chunks, every chunk but the last
 // of a row from an empty state, without C, z or outputs.  Otherwise the pass that
-// writes the outputs; a chunk's start is folded from the summaries before it.
-template <typename T, int N, int NS, int V, bool SUMMARY>
-__global__ void __launch_bounds__(kScanThreads)
+// writes the outputs; k_scan_chain has turned the summaries' ends into the ends
+// of the whole row up to each chunk.
+//
+// A tile passes through three steps: every thread turns 8 elements (token,
+// channel) into dt and dt u in shared memory; the state lanes walk the tile's
+// tokens and leave y there; every thread turns its elements' y into outputs.  The
+// elements come by 16-byte asynchronous copies, two tiles deep, each thread
+// copying what it alone reads (no barrier between them); rows that do not start on 16
+// bytes go through registers one tile ahead.
+// Channel cl of a tile sits at place (cl % V) CV + cl / V of a shared row, so
+// that the V channels of a thread's access land V different rows' width apart
+// and neighbouring threads write neighbouring words; the state lanes take the
+// places in order.
+template <typename T, int N, int V, bool SUMMARY>
+struct ScanShared {
+    static constexpr int LPC = N / kScanNS, CPB = kScanThreads * kScanCH / LPC;
+    static constexpr int EPT = V > 1 ? 32 / (int)sizeof(T) : 8;        // elements a thread, two copies of 16 bytes
+    static constexpr int TT = EPT * kScanThreads / CPB, NV = EPT / V, CV = CPB / V;
+    static constexpr int NT = SUMMARY ? 2 : 3, NM = SUMMARY ? 1 : 2;   // element tensors; B (and C)
+    static constexpr int BV = V > 1 ? 16 / (int)sizeof(T) : 1;         // elements of B and C a copy
+    static constexpr int BC = TT * N / BV, EB = (BC + kScanThreads - 1) / kScanThreads;
+    Pack<T, V> raw[2][NT][NV][kScanThreads];
+    Pack<T, BV> rawbc[2][NM][EB][kScanThreads];
+    static constexpr int PAD = CV < 32 ? (CV < 2 ? 2 : CV) : 0;   // the rows that one warp's element lanes touch start on other banks
+    alignas(16) float2 sdt[TT][CPB + PAD];      // (dt, dt u), then (y, )
+    alignas(16) float sbias[CV][V], sskip[CV][V];
+    alignas(16) float bc[NM][TT][N];
+};
+
+template <typename T, int N, int V, bool SUMMARY>
+__global__ void __launch_bounds__(kScanThreads, kScanPerSm)
 k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
-    constexpr int LPC = N / NS, CPB = kScanThreads / LPC, TT = 8 * LPC, NV = 8 / V, CV = CPB / V;
-    constexpr int EB = TT * N / kScanThreads > 0 ? TT * N / kScanThreads : 1;
-    __shared__ float2 sdt[TT][CPB];             // (dt, dt u); .x becomes y
-    __shared__ __align__(16) float sB[TT][N];
-    __shared__ __align__(16) float sC[TT][N];
+    using S = ScanShared<T, N, V, SUMMARY>;
+    constexpr int LPC = S::LPC, CPB = S::CPB, TT = S::TT, NV = S::NV, CV = S::CV, BV = S::BV, BC = S::BC, EB = S::EB;
+    constexpr int NS = kScanNS, CH = kScanCH;
+    constexpr int GK = LPC < 2 ? 1 : LPC / 2;   // tokens whose y are summed over the lanes together: LPC values
+    constexpr int UN = GK < 4 ? 4 : GK;         // tokens a step of the walk
+    extern __shared__ __align__(16) unsigned char smem[];
+    S& sm = *reinterpret_cast<S*>(smem);
 
     const int tile = blockIdx.x % pl.tiles, rest = blockIdx.x / pl.tiles;
     const int b = rest % p.B, chunk = rest / p.B;
@@ -87,161 +107,280 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     const T* Bm = (const T*)p.Bm + (row * G + g) * N;
     const T* Cm = (const T*)p.Cm + (row * G + g) * N;
 
-    // state lanes: channel ch, states part*NS .. +NS-1
-    const int ch = threadIdx.x / LPC, part = threadIdx.x % LPC;
-    const bool live = ch < cn;
-    uint64_t A2[NS / 2], h[NS / 2];
-    const size_t cn0 = (size_t)(c0 + (live ? ch : 0)) * N + part * NS;
-#pragma unroll
-    for (int n = 0; n < NS / 2; ++n)
-        A2[n] = pack2(p.A[cn0 + 2 * n] * kLog2e, p.A[cn0 + 2 * n + 1] * kLog2e);
-    float* stp = p.state ? p.state + (size_t)page * D * N + cn0 : nullptr;
-#pragma unroll
-    for (int n = 0; n < NS / 2; ++n)
-        h[n] = stp && chunk == 0 && (SUMMARY || t1 == len) ? *reinterpret_cast<const uint64_t*>(stp + 2 * n) : 0ull;
-    if (SUMMARY && stp && chunk == 0) {
-#pragma unroll
-        for (int n = 0; n < NS / 2; ++n)
-            if (live) *reinterpret_cast<uint64_t*>(ws.h0 + (size_t)b * D * N + cn0 + 2 * n) = h[n];
-    }
-    if (!SUMMARY && stp && chunk == 0 && t1 < len) {
-#pragma unroll
-        for (int n = 0; n < NS / 2; ++n) h[n] = *reinterpret_cast<const uint64_t*>(ws.h0 + (size_t)b * D * N + cn0 + 2 * n);
-    }
-    if (!SUMMARY && chunk > 0) {
-        // the chunks before, from the row's start (which chunk 0's end holds already)
-#pragma unroll 4
-        for (int j = 0; j < chunk; ++j) {
-            const size_t r = ((size_t)b * pl.nC + j) * D;
-            const float s = ws.sdt[r + c0 + (live ? ch : 0)];
-            const uint64_t s2 = pack2(s, s);
-#pragma unroll
-            for (int n = 0; n < NS / 2; ++n) {
-                const uint64_t e = *reinterpret_cast<const uint64_t*>(ws.hend + r * N + cn0 + 2 * n);
-                h[n] = fma2(ex2_2(mul2(A2[n], s2)), h[n], e);
-            }
-        }
-    }
-    float total_dt = 0.f;
-
     // element lanes: vector v is V channels of one token of the tile
     int ev_t[NV], ev_c[NV];
-    float bias[NV][V], skip[NV][V];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int i = v * kScanThreads + threadIdx.x;
         ev_t[v] = i / CV;
-        ev_c[v] = i % CV * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const bool ok = ev_c[v] + e < cn;
-            bias[v][e] = ok && p.dt_bias ? p.dt_bias[c0 + ev_c[v] + e] : 0.f;
-            skip[v][e] = ok && p.skip && !SUMMARY ? p.skip[c0 + ev_c[v] + e] : 0.f;
-        }
+        ev_c[v] = i % CV;
     }
-    Pack<T, V> ru[NV], rd[NV], rz[NV];
-    T rB[EB], rC[EB];
-    auto fetch = [&](int t) {
+    // registers of the narrow path, one tile ahead of the shared slots
+    Pack<T, V> rr[V == 1 ? S::NT : 1][V == 1 ? NV : 1];
+    T rbc[V == 1 ? S::NM : 1][V == 1 ? EB : 1];
+    auto fetch = [&](int t, int slot) {
+        const T* src[3] = {u, dt, z};
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const bool ok = t + ev_t[v] < t1 && ev_c[v] < cn;
-            const size_t at = (size_t)(t + ev_t[v]) * D + ev_c[v];
-            ru[v] = ok ? load_pack<T, V>(u + at) : zero_pack<T, V>();
-            rd[v] = ok ? load_pack<T, V>(dt + at) : zero_pack<T, V>();
-            if (!SUMMARY) rz[v] = ok && z ? load_pack<T, V>(z + at) : zero_pack<T, V>();
-        }
+        for (int k = 0; k < S::NT; ++k)
 #pragma unroll
-        for (int i = 0; i < EB; ++i) {
-            const int e = i * kScanThreads + threadIdx.x, tt = e / N, n = e % N;
-            const bool ok = tt < TT && t + tt < t1;
-            const size_t at = (size_t)(t + tt) * G * N + n;
-            from_f(rB[i], 0.f);
-            from_f(rC[i], 0.f);
-            if (ok) rB[i] = Bm[at];
-            if (ok && !SUMMARY) rC[i] = Cm[at];
+            for (int v = 0; v < NV; ++v) {
+                const bool ok = t + ev_t[v] < t1 && ev_c[v] * V < cn && (k < 2 || z);
+                const T* at = ok ? src[k] + (size_t)(t + ev_t[v]) * D + ev_c[v] * V : u;
+                if constexpr (V > 1) {
+                    copy16_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
+                } else {
+                    rr[k][v] = ok ? load_pack<T, V>(at) : zero_pack<T, V>();
+                }
+            }
+        const T* mat[2] = {Bm, Cm};
+#pragma unroll
+        for (int k = 0; k < S::NM; ++k)
+#pragma unroll
+            for (int i = 0; i < EB; ++i) {
+                const int e = i * kScanThreads + threadIdx.x, tt = e / (N / BV), n = e % (N / BV) * BV;
+                const bool ok = e < BC && t + tt < t1;
+                const T* at = ok ? mat[k] + (size_t)(t + tt) * G * N + n : mat[k];
+                if constexpr (V > 1) {
+                    if (e < BC) copy16_async(&sm.rawbc[slot][k][i][threadIdx.x], at, ok);
+                } else {
+                    from_f(rbc[k][i], 0.f);
+                    if (ok) rbc[k][i] = *at;
+                }
+            }
+        if constexpr (V > 1) copy_commit();
+    };
+    // the tile's elements are in this thread's slots
+    auto arrive = [&](int slot) {
+        if constexpr (V > 1) {
+            copy_wait<1>();
+        } else {
+#pragma unroll
+            for (int k = 0; k < S::NT; ++k)
+#pragma unroll
+                for (int v = 0; v < NV; ++v) sm.raw[slot][k][v][threadIdx.x] = rr[k][v];
+#pragma unroll
+            for (int k = 0; k < S::NM; ++k)
+#pragma unroll
+                for (int i = 0; i < EB; ++i) sm.rawbc[slot][k][i][threadIdx.x].v[0] = rbc[k][i];
         }
     };
-    fetch(t0);
-    for (int t = t0; t < t1; t += TT) {
-        const int nt = min(TT, t1 - t);
-        Pack<T, V> cu[NV], cz[NV];
+    fetch(t0, 0);
+    if constexpr (V > 1) fetch(t0 + TT, 1);
+
+    // state lanes: the channels at places 2q and 2q + 1, states part*8 .. +7
+    const int q = threadIdx.x / LPC, part = threadIdx.x % LPC;
+    int ch[CH];
+    bool live[CH];
+    size_t cn0[CH];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = softplus_f(to_f(rd[v].v[e]) + bias[v][e]);
-                sdt[ev_t[v]][ev_c[v] + e] = make_float2(d, d * to_f(ru[v].v[e]));
-            }
-            cu[v] = ru[v];
-            cz[v] = rz[v];
+    for (int c = 0; c < CH; ++c) {
+        const int at = q * CH + c;
+        ch[c] = at % CV * V + at / CV;
+        live[c] = ch[c] < cn;
+        if (!live[c]) ch[c] = 0;
+        cn0[c] = (size_t)(c0 + ch[c]) * N + part * NS;
+        if (part == 0) {
+            sm.sbias[at % CV][at / CV] = live[c] && p.dt_bias ? p.dt_bias[c0 + ch[c]] : 0.f;
+            sm.sskip[at % CV][at / CV] = live[c] && p.skip ? p.skip[c0 + ch[c]] : 0.f;
         }
+    }
+    uint64_t A2[CH][NS / 2], h[CH][NS / 2];
+    const uint64_t mean2 = pack2(kEx2Mean, kEx2Mean);
+    float* stp = p.state ? p.state + (size_t)page * D * N : nullptr;
+    float* h0p = ws.h0 + (size_t)b * D * N;
+    // The page's state: read here by the pass that does not write pages, unless chunk 0 is all of the row.
+    const float* start = SUMMARY || t1 == len ? stp : h0p;
+    if (chunk) start = SUMMARY ? nullptr : ws.hend + ((size_t)b * pl.nC + chunk - 1) * D * N;
+    else if (!stp) start = nullptr;
 #pragma unroll
-        for (int i = 0; i < EB; ++i) {
-            const int e = i * kScanThreads + threadIdx.x, tt = e / N, n = e % N;
-            if (tt < TT) {
-                sB[tt][n] = to_f(rB[i]);
-                if (!SUMMARY) sC[tt][n] = to_f(rC[i]);
-            }
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int n = 0; n < NS / 2; ++n) {
+            A2[c][n] = pack2(p.A[cn0[c] + 2 * n] * kLog2e, p.A[cn0[c] + 2 * n + 1] * kLog2e);
+            h[c][n] = start ? *reinterpret_cast<const uint64_t*>(start + cn0[c] + 2 * n) : 0ull;
+            if (SUMMARY && start && live[c]) *reinterpret_cast<uint64_t*>(h0p + cn0[c] + 2 * n) = h[c][n];
         }
-        __syncthreads();
-        if (t + TT < t1) fetch(t + TT);
-#pragma unroll 4
-        for (int tt = 0; tt < nt; ++tt) {
-            const float2 dd = sdt[tt][ch];
-            const uint64_t d2 = pack2(dd.x, dd.x), x2 = pack2(dd.y, dd.y);
-            uint64_t y2 = 0;
-            const ulonglong2* B2 = reinterpret_cast<const ulonglong2*>(&sB[tt][part * NS]);
-            const ulonglong2* C2 = reinterpret_cast<const ulonglong2*>(&sC[tt][part * NS]);
+    float total_dt[CH] = {};
+
+    // K tokens from tt on: the states move on, the lane's part of their y comes back, token by
+    // token its channels.  The decays do not wait for the states, so they are formed first.
+    auto tokens = [&](int tt, auto kc, float* y) {
+        constexpr int K = decltype(kc)::value;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float4 d4 = *reinterpret_cast<const float4*>(&sm.sdt[tt + k][q * CH]);
+            const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w};
+            uint64_t a[CH][NS / 2];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint64_t d2 = pack2(dd[c], dd[c]);
+#pragma unroll
+                for (int n = 0; n < NS / 2; ++n) a[c][n] = ex2_2(fma2(A2[c][n], d2, mean2));
+                if (SUMMARY) total_dt[c] += dd[c];
+            }
+            const ulonglong2* B2 = reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt + k][part * NS]);
+            const ulonglong2* C2 = reinterpret_cast<const ulonglong2*>(&sm.bc[S::NM - 1][tt + k][part * NS]);
+            uint64_t y2[CH], x2[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) x2[c] = pack2(xx[c], xx[c]);
 #pragma unroll
             for (int n = 0; n < NS / 4; ++n) {
                 const ulonglong2 bb = B2[n];
-                h[2 * n] = fma2(ex2_2(mul2(A2[2 * n], d2)), h[2 * n], mul2(x2, bb.x));
-                h[2 * n + 1] = fma2(ex2_2(mul2(A2[2 * n + 1], d2)), h[2 * n + 1], mul2(x2, bb.y));
-                if (!SUMMARY) {
-                    const ulonglong2 cc = C2[n];
-                    y2 = fma2(h[2 * n], cc.x, y2);
-                    y2 = fma2(h[2 * n + 1], cc.y, y2);
+                ulonglong2 cc;
+                if (!SUMMARY) cc = C2[n];
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    h[c][2 * n] = fma2(a[c][2 * n], h[c][2 * n], mul2(x2[c], bb.x));
+                    h[c][2 * n + 1] = fma2(a[c][2 * n + 1], h[c][2 * n + 1], mul2(x2[c], bb.y));
+                    if (!SUMMARY) {
+                        y2[c] = n ? fma2(h[c][2 * n], cc.x, y2[c]) : mul2(h[c][2 * n], cc.x);
+                        y2[c] = fma2(h[c][2 * n + 1], cc.y, y2[c]);
+                    }
                 }
             }
-            if (SUMMARY) {
-                total_dt += dd.x;
-            } else {
-                float y0, y1;
-                unpack2(y2, y0, y1);
-                float y = y0 + y1;
+            if (!SUMMARY) {
 #pragma unroll
-                for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                if (part == 0) sdt[tt][ch].x = y;
+                for (int c = 0; c < CH; ++c) {
+                    float y0, y1;
+                    unpack2(y2[c], y0, y1);
+                    y[k * CH + c] = y0 + y1;
+                }
             }
+        }
+    };
+    // y of GK tokens from tt on, summed over a channel's lanes: at each bit of part a lane keeps
+    // half of its values, the upper half where the bit is set.
+    auto finish = [&](int tt, float* y, int nt) {
+        if constexpr (LPC == 1) {
+            sm.sdt[tt][q * CH].x = y[0];
+            sm.sdt[tt][q * CH + 1].x = y[1];
+        } else {
+            int k = 0;
+#pragma unroll
+            for (int o = 1, w = LPC / 2; o < LPC; o <<= 1, w >>= 1) {
+                const bool up = part & o;
+#pragma unroll
+                for (int i = 0; i < w; ++i) {
+                    const float keep = up ? y[i + w] : y[i], give = up ? y[i] : y[i + w];
+                    y[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+                k += up ? w : 0;
+            }
+            if (GK == 1 || tt + k / CH < nt) sm.sdt[tt + k / CH][q * CH + k % CH].x = y[0];
+        }
+    };
+
+    auto bias_of = [](const float (&f)[V]) {
+        Pack<float, V> r;
+        if constexpr (V >= 4) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(&r.v[i]) = *reinterpret_cast<const float4*>(&f[i]);
+        } else {
+            r.v[0] = f[0];
+        }
+        return r;
+    };
+    int slot = 0;
+    for (int t = t0; t < t1; t += TT, slot ^= 1) {
+        const int nt = min(TT, t1 - t);
+        if (t == t0) __syncthreads();           // sbias
+        arrive(slot);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const Pack<T, V> ru = sm.raw[slot][0][v][threadIdx.x], rd = sm.raw[slot][1][v][threadIdx.x];
+            const Pack<float, V> bias = bias_of(sm.sbias[ev_c[v]]);
+            float d[V + V % 2];
+            if constexpr (V == 1) d[1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] = to_f(rd.v[e]) + bias.v[e];
+#pragma unroll
+            for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                sm.sdt[ev_t[v]][e * CV + ev_c[v]] = make_float2(d[e], d[e] * to_f(ru.v[e]));
+        }
+#pragma unroll
+        for (int k = 0; k < S::NM; ++k)
+#pragma unroll
+            for (int i = 0; i < EB; ++i) {
+                const int e = i * kScanThreads + threadIdx.x;
+                if (e < BC) {
+                    const Pack<T, BV> m = sm.rawbc[slot][k][i][threadIdx.x];
+                    float* to = &sm.bc[k][0][0] + e * BV;
+#pragma unroll
+                    for (int x = 0; x < BV; ++x) to[x] = to_f(m.v[x]);
+                }
+            }
+        __syncthreads();
+        if constexpr (V == 1) fetch(t + TT, 0);
+        int tt = 0;
+        for (; tt + UN <= nt; tt += UN) {
+            float y[UN * CH];
+            tokens(tt, std::integral_constant<int, UN>(), y);
+            if (!SUMMARY) {
+#pragma unroll
+                for (int k = 0; k < UN; k += GK) finish(tt + k, y + k * CH, nt);
+            }
+        }
+        for (; tt < nt; tt += GK) {
+            float y[GK * CH] = {};
+#pragma unroll
+            for (int k = 0; k < GK; ++k)
+                if (tt + k < nt) tokens(tt + k, std::integral_constant<int, 1>(), y + k * CH);
+            if (!SUMMARY) finish(tt, y, nt);
         }
         __syncthreads();
         if (!SUMMARY) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (ev_t[v] >= nt || ev_c[v] >= cn) continue;
+                if (ev_t[v] >= nt || ev_c[v] * V >= cn) continue;
+                const Pack<T, V> ru = sm.raw[slot][0][v][threadIdx.x], rz = sm.raw[slot][S::NT - 1][v][threadIdx.x];
+                const Pack<float, V> skip = bias_of(sm.sskip[ev_c[v]]);
                 Pack<T, V> o;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float y = fmaf(skip[v][e], to_f(cu[v].v[e]), sdt[ev_t[v]][ev_c[v] + e].x);
+                    float y = fmaf(skip.v[e], to_f(ru.v[e]), sm.sdt[ev_t[v]][e * CV + ev_c[v]].x);
                     if (z) {
-                        const float zz = to_f(cz[v].v[e]);
+                        const float zz = to_f(rz.v[e]);
                         y *= zz * sigmoid_f<T>(zz);
                     }
                     from_f(o.v[e], y);
                 }
-                *reinterpret_cast<Pack<T, V>*>(out + (size_t)(t + ev_t[v]) * D + ev_c[v]) = o;
+                *reinterpret_cast<Pack<T, V>*>(out + (size_t)(t + ev_t[v]) * D + ev_c[v] * V) = o;
             }
         }
+        if constexpr (V > 1) fetch(t + 2 * TT, slot);
     }
-    if (!live) return;
-    if (SUMMARY) {
+    if constexpr (V > 1) copy_wait<0>();
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if (!live[c]) continue;
         const size_t r = ((size_t)b * pl.nC + chunk) * D;
+        float* to = SUMMARY ? ws.hend + r * N : stp && t1 == len ? stp : nullptr;
 #pragma unroll
-        for (int n = 0; n < NS / 2; ++n) *reinterpret_cast<uint64_t*>(ws.hend + r * N + cn0 + 2 * n) = h[n];
-        if (part == 0) ws.sdt[r + c0 + ch] = total_dt;
-    } else if (stp && t1 == len) {
-#pragma unroll
-        for (int n = 0; n < NS / 2; ++n) *reinterpret_cast<uint64_t*>(stp + 2 * n) = h[n];
+        for (int n = 0; n < NS / 2; ++n)
+            if (to) *reinterpret_cast<uint64_t*>(to + cn0[c] + 2 * n) = h[c][n];
+        if (SUMMARY && part == 0) ws.sdt[r + c0 + ch[c]] = total_dt[c];
+    }
+}
+
+// Per (row, channel, state): h <- decay of the chunk h + the chunk's own end, in the
+// chunks' order (chunk 0's end holds the row's start already).
+__global__ void __launch_bounds__(128) k_scan_chain(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int N) {
+    const size_t i = (size_t)blockIdx.x * 128 + threadIdx.x, DN = (size_t)D * N;
+    if (i >= (size_t)p.B * DN) return;
+    const int b = (int)(i / DN);
+    const size_t cn = i % DN;
+    const int c = (int)(cn / N), used = (row_len(p.lens, b, p.L) + pl.Lc - 1) / pl.Lc;   // the last one gave no summary
+    const float A = p.A[cn] * kLog2e;
+    float* hend = ws.hend + (size_t)b * pl.nC * DN + cn;
+    const float* sdt = ws.sdt + (size_t)b * pl.nC * D + c;
+    if (used < 2) return;
+    float h = hend[0];
+#pragma unroll 8
+    for (int j = 1; j < used - 1; ++j) {
+        h = fmaf(ex2_approx(A * sdt[(size_t)j * D]), h, hend[(size_t)j * DN]);
+        hend[(size_t)j * DN] = h;
     }
 }
 
@@ -274,10 +413,10 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanArgs p, int D, i
     float4* sp = reinterpret_cast<float4*>(p.state + ((size_t)page * D + cc) * N + part * 4);
     float4 h = *sp;
     const float d = softplus_f(raw), x = d * uu, dl = d * kLog2e;
-    h.x = fmaf(ex2_approx(a0 * dl), h.x, x * bm[0]);
-    h.y = fmaf(ex2_approx(a1 * dl), h.y, x * bm[1]);
-    h.z = fmaf(ex2_approx(a2 * dl), h.z, x * bm[2]);
-    h.w = fmaf(ex2_approx(a3 * dl), h.w, x * bm[3]);
+    h.x = fmaf(ex2_approx(fmaf(a0, dl, kEx2Mean)), h.x, x * bm[0]);
+    h.y = fmaf(ex2_approx(fmaf(a1, dl, kEx2Mean)), h.y, x * bm[1]);
+    h.z = fmaf(ex2_approx(fmaf(a2, dl, kEx2Mean)), h.z, x * bm[2]);
+    h.w = fmaf(ex2_approx(fmaf(a3, dl, kEx2Mean)), h.w, x * bm[3]);
     if (in) *sp = h;
     float y = fmaf(h.x, cm[0], h.y * cm[1]) + fmaf(h.z, cm[2], h.w * cm[3]);
 #pragma unroll
@@ -290,49 +429,54 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanArgs p, int D, i
 }
 
 // ------------------------------------------------------------------ launches
-template <int N> struct ScanNS { static constexpr int value = N < 16 ? N : 16; };
-
-// Blocks that a call should have before its tokens are cut into chunks: cutting
-// runs every exponential twice.
-static int scan_target(const SsmHandle& h) { return h.num_sms * 8; }
+// Cutting the tokens into chunks fills the SMs, but runs every exponential of all
+// but the last chunk twice: with room for 3 chunks or more it pays (1024 tokens,
+// 192 blocks of channels: 205 us in 3 chunks, 227 uncut), with 2 it does not
+// (256 blocks: 271 and 227 us).  A chunk is 64 tokens at least.
 constexpr int kScanMinChunk = 64;
 
-template <int N>
-static ScanPlan scan_plan(const SsmHandle& h, int B, int L) {
-    constexpr int LPC = N / ScanNS<N>::value, CPB = kScanThreads / LPC, TT = 8 * LPC;
+static ScanPlan scan_plan(const SsmHandle& h, int B, int L, int CPB, int TT) {
     ScanPlan pl;
     pl.Dg = h.D / h.G;
     pl.tpg = (pl.Dg + CPB - 1) / CPB;
     pl.tiles = pl.tpg * h.G;
-    const long long blocks = (long long)pl.tiles * B;
-    long long want = scan_target(h) / blocks;
+    long long want = (long long)h.num_sms * kScanPerSm / ((long long)pl.tiles * B);
     const int most = (L + kScanMinChunk - 1) / kScanMinChunk;
+    if (want < 3) want = 1;
     if (want > most) want = most;
-    if (want < 1) want = 1;
     pl.Lc = (int)((L + want - 1) / want);
     pl.Lc = (pl.Lc + TT - 1) / TT * TT;
     pl.nC = (L + pl.Lc - 1) / pl.Lc;
     return pl;
 }
 
-// Several chunks come only while tiles * B * chunks <= scan_target, each of at
-// most 128 channels.
-size_t scan_prompt_ws(const SsmHandle& h) { return (size_t)scan_target(h) * kScanThreads * (2 * h.N + 1); }
+// Several chunks come only while tiles * B * chunks <= SMs * kScanPerSm; a tile has
+// 128 * 16 states and at most 256 channels.
+size_t scan_prompt_ws(const SsmHandle& h) {
+    return (size_t)h.num_sms * kScanPerSm * (2 * kScanThreads * kScanNS * kScanCH + 256);
+}
 
 template <typename T, int N, int V>
 static void scan_launch(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
-    constexpr int NS = ScanNS<N>::value;
-    const ScanPlan pl = scan_plan<N>(h, a.B, a.L);
+    using S = ScanShared<T, N, V, false>;
+    const ScanPlan pl = scan_plan(h, a.B, a.L, S::CPB, S::TT);
     ScanWs ws;
     ws.hend = h.ws;
     ws.h0 = ws.hend + (size_t)a.B * pl.nC * h.D * N;
     ws.sdt = ws.h0 + (size_t)a.B * h.D * N;
+    auto launch = [&](auto kernel, size_t smem, int chunks) {
+        // the attribute's failure shows as the launch's
+        if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        kernel<<<(unsigned)pl.tiles * a.B * chunks, kScanThreads, smem, st>>>(a, pl, ws, h.D, h.G);
+        count_launch();
+    };
     if (pl.nC > 1) {
-        k_scan<T, N, NS, V, true><<<(unsigned)pl.tiles * a.B * (pl.nC - 1), kScanThreads, 0, st>>>(a, pl, ws, h.D, h.G);
+        launch(k_scan<T, N, V, true>, sizeof(ScanShared<T, N, V, true>), pl.nC - 1);
+        const size_t n = (size_t)a.B * h.D * N;
+        k_scan_chain<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(a, pl, ws, h.D, N);
         count_launch();
     }
-    k_scan<T, N, NS, V, false><<<(unsigned)pl.tiles * a.B * pl.nC, kScanThreads, 0, st>>>(a, pl, ws, h.D, h.G);
-    count_launch();
+    launch(k_scan<T, N, V, false>, sizeof(ScanShared<T, N, V, false>), pl.nC);
 }
 
 template <typename T, int V>
@@ -346,9 +490,9 @@ static void scan_by_n(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
 favor_status scan_prompt(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
     const bool f32 = h.dtype == FAVOR_DTYPE_F32;
     const int v = f32 ? 4 : 8;
-    // 16-byte accesses of u, dt, z, out need every row of a group to start on one
+    // 16-byte accesses need every row of a group to start on one (rows of B and C are N >= 8 elements)
     const bool vec = h.D % v == 0 && (h.D / h.G) % v == 0 && is_aligned16(a.u) && is_aligned16(a.dt) &&
-                     is_aligned16(a.z) && is_aligned16(a.out);
+                     is_aligned16(a.z) && is_aligned16(a.out) && is_aligned16(a.Bm) && is_aligned16(a.Cm);
     if (f32 && vec) scan_by_n<float, 4>(h, a, st);
     else if (f32) scan_by_n<float, 1>(h, a, st);
     else if (vec) scan_by_n<__nv_bfloat16, 8>(h, a, st);
