@@ -2,10 +2,11 @@
 //     p[t, c] = bias[c] + sum_k w[c, k] x[t - K + 1 + k, c],   out = p or p * sigmoid(p)
 // with the inputs before the first token taken from a window page [K-1, D]
 // (zeros without one).  Nothing but bytes: 2K + 5 operations an element against
-// one read and one write, so a thread owns a 16-byte column of channels (one
-// channel where the rows do not start on 16 bytes) for a run of tokens, loads
-// the run's rows up front and keeps them in registers; only the K-1 rows before
-// a run are read twice (from L2).
+// one read and one write.  A thread owns 4 neighbouring channels (one where the
+// rows do not start on 16 bytes) for a run of tokens, the filter in registers; the
+// run's rows come through asynchronous copies, some tokens deep, into slots that
+// only their thread reads, so that the bytes in flight cost no registers.  Only the
+// K-1 rows before a run are read twice (from L2).
 #include <initializer_list>
 
 #include "ssm_internal.h"
@@ -27,48 +28,77 @@ __device__ __forceinline__ float dsilu_f(float p) {
 template <int V, int K>
 __device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c, float (&w)[V][K],
                                           float (&b)[V]) {
+    if constexpr (V >= 4) {   // 16 bytes at a time: c is a multiple of V
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < V * K; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(weight + (size_t)c * K + i);
+            w[i / K][i % K] = f.x;
+            w[(i + 1) / K][(i + 1) % K] = f.y;
+            w[(i + 2) / K][(i + 2) % K] = f.z;
+            w[(i + 3) / K][(i + 3) % K] = f.w;
+        }
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[i][k] = weight[(size_t)(c + i) * K + k];
-        b[i] = bias ? bias[c + i] : 0.f;
+        for (int i = 0; i < V; i += 4) {
+            const float4 f = bias ? *reinterpret_cast<const float4*>(bias + c + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            b[i] = f.x;
+            b[i + 1] = f.y;
+            b[i + 2] = f.z;
+            b[i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[0][k] = weight[(size_t)c * K + k];
+        b[0] = bias ? bias[c] : 0.f;
     }
 }
 
-// Grid: channel blocks x runs x rows.  A run is R tokens.
-template <typename T, int V, int K, int R>
-__global__ void __launch_bounds__(kConvThreads) k_conv(ConvArgs a, int D, int cblocks, int runs) {
+// Grid: channel blocks x runs x rows.  A run of R tokens is walked 8 at a time (4 in
+// fp32), the two steps after it in flight.  [4, 8192, 1024] bf16: 34 us (4.0 TB/s; 43
+// with the next rows in registers, 55 with 8 tokens a thread and no overlap).
+constexpr int kConvStages = 3;
+
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kConvThreads) k_conv(ConvArgs a, int D, int cblocks, int runs, int R) {
+    constexpr int U = sizeof(T) == 4 ? 4 : 8;
     const int cb = blockIdx.x % cblocks, rest = blockIdx.x / cblocks;
     const int run = rest % runs, b = rest / runs;
     const int page = a.window ? block_page(a.pg, b) : 0;
     const int len = row_len(a.lens, b, a.L);
-    const int t0 = run * R, n = min(R, len - t0);
+    const int t0 = run * R, t1 = min(len, t0 + R);
     const int c = (cb * kConvThreads + threadIdx.x) * V;
-    if (n <= 0 || c >= D) return;
+    if (t0 >= t1 || c >= D) return;
     const T* x = (const T*)a.x + (size_t)b * a.L * D + c;
     T* out = (T*)a.out + (size_t)b * a.L * D + c;
     if (page < 0) {   // the row takes no part
-        for (int i = 0; i < n; ++i) *reinterpret_cast<Pack<T, V>*>(out + (size_t)(t0 + i) * D) = zero_pack<T, V>();
+        for (int t = t0; t < t1; ++t) *reinterpret_cast<Pack<T, V>*>(out + (size_t)t * D) = zero_pack<T, V>();
         return;
     }
     T* win = a.window ? (T*)a.window + (size_t)page * (K - 1) * D + c : nullptr;
     float w[V][K], bias[V];
+    __shared__ Pack<T, V> ring[V > 1 ? kConvStages : 1][U][kConvThreads];
+    Pack<T, V> r[U + K - 1], ahead[V > 1 ? 1 : U];   // rows t-K+1 .. t+7; narrow rows: t+8 ..
+    auto fetch = [&](int t, int slot) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const bool ok = t + i < t1;
+            if constexpr (V > 1) copy_async(&ring[slot][i][threadIdx.x], ok ? x + (size_t)(t + i) * D : x, ok);
+            else ahead[i] = ok ? load_pack<T, V>(x + (size_t)(t + i) * D) : zero_pack<T, V>();
+        }
+        if constexpr (V > 1) copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < (V > 1 ? kConvStages - 1 : 1); ++s) fetch(t0 + s * U, s);
     load_taps<V, K>(a.weight, a.bias, c, w, bias);
-    // rows t0-K+1 .. t0+R-1
-    Pack<T, V> r[R + K - 1];
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
         const int t = t0 - (K - 1) + i;
         r[i] = t >= 0 ? load_pack<T, V>(x + (size_t)t * D)
                       : win ? load_pack<T, V>(win + (size_t)(t + K - 1) * D) : zero_pack<T, V>();
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        r[K - 1 + i] = i < n ? load_pack<T, V>(x + (size_t)(t0 + i) * D) : zero_pack<T, V>();
     // The first run alone reads the window, so its thread also moves it on: the
     // last K-1 of (window, inputs), row K-1 + len - (K-1) + i = len + i of that list.
-    Pack<T, V> last[K - 1];
     if (win && run == 0) {
+        Pack<T, V> last[K - 1];
 #pragma unroll
         for (int i = 0; i < K - 1; ++i) {
             const int t = len - (K - 1) + i;
@@ -77,19 +107,35 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvArgs a, int D, int cb
 #pragma unroll
         for (int i = 0; i < K - 1; ++i) *reinterpret_cast<Pack<T, V>*>(win + (size_t)i * D) = last[i];
     }
+    int slot = 0;
+    for (int t = t0; t < t1; t += U) {
+        if constexpr (V > 1) copy_wait<kConvStages - 2>();
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        if (i >= n) break;
-        Pack<T, V> o;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float p = bias[e];
-#pragma unroll
-            for (int k = 0; k < K; ++k) p = fmaf(w[e][k], to_f(r[i + k].v[e]), p);
-            from_f(o.v[e], a.silu ? silu_f<T>(p) : p);
+        for (int i = 0; i < U; ++i) {
+            if constexpr (V > 1) r[K - 1 + i] = ring[slot][i][threadIdx.x];
+            else r[K - 1 + i] = ahead[i];
         }
-        *reinterpret_cast<Pack<T, V>*>(out + (size_t)(t0 + i) * D) = o;
+        // the slot before this one was read in the last step
+        if constexpr (V > 1) fetch(t + (kConvStages - 1) * U, slot ? slot - 1 : kConvStages - 1);
+        else fetch(t + U, 0);
+        slot = slot + 1 < kConvStages ? slot + 1 : 0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (t + i >= t1) break;
+            Pack<T, V> o;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float p = bias[e];
+#pragma unroll
+                for (int k = 0; k < K; ++k) p = fmaf(w[e][k], to_f(r[i + k].v[e]), p);
+                from_f(o.v[e], a.silu ? silu_f<T>(p) : p);
+            }
+            *reinterpret_cast<Pack<T, V>*>(out + (size_t)(t + i) * D) = o;
+        }
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) r[i] = r[U + i];
     }
+    if constexpr (V > 1) copy_wait<0>();
 }
 
 // One token a row: x [B, D], the window moves on by one.
@@ -97,20 +143,24 @@ template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvArgs a, int D, int cblocks) {
     const int cb = blockIdx.x % cblocks, b = blockIdx.x / cblocks;
     const int c = (cb * kConvThreads + threadIdx.x) * V;
-    const int page = block_page(a.pg, b);
-    if (c >= D) return;
+    int page = row_page(a.pg, b);
+    const bool in = c < D;
+    T* win = (T*)a.window + (size_t)(page < 0 ? 0 : page) * (K - 1) * D + (in ? c : 0);
     T* out = (T*)a.out + (size_t)b * D + c;
+    Pack<T, V> r[K];
+    float w[V][K], bias[V];
+    if (in) {   // in flight while the earlier rows are looked through
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) r[i] = load_pack<T, V>(win + (size_t)i * D);
+        r[K - 1] = load_pack<T, V>((const T*)a.x + (size_t)b * D + c);
+        load_taps<V, K>(a.weight, a.bias, c, w, bias);
+    }
+    if (block_page_taken(a.pg, b, page)) page = -1;
+    if (!in) return;
     if (page < 0) {   // the row takes no part
         *reinterpret_cast<Pack<T, V>*>(out) = zero_pack<T, V>();
         return;
     }
-    T* win = (T*)a.window + (size_t)page * (K - 1) * D + c;
-    Pack<T, V> r[K];
-#pragma unroll
-    for (int i = 0; i < K - 1; ++i) r[i] = load_pack<T, V>(win + (size_t)i * D);
-    r[K - 1] = load_pack<T, V>((const T*)a.x + (size_t)b * D + c);
-    float w[V][K], bias[V];
-    load_taps<V, K>(a.weight, a.bias, c, w, bias);
     Pack<T, V> o;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -162,39 +212,79 @@ k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
             }
         }
     }
-    for (int t = t0; t < t1 + K - 1 && t0 < t1; ++t) {
-        const bool in = t < len;
-        const Pack<T, V> rx = in ? load_pack<T, V>(x + (size_t)t * D) : zero_pack<T, V>();
-        const Pack<T, V> rg = in ? load_pack<T, V>(dout + (size_t)t * D) : zero_pack<T, V>();
-        const bool own = t < t1;
-        Pack<T, V> o;
+    constexpr int U = 4, STAGES = 3;   // tokens a step, steps in the ring
+    __shared__ Pack<T, V> ring[V > 1 ? STAGES : 1][2][U][kConvThreads];
+    Pack<T, V> ahead[2][V > 1 ? 1 : U];
+    const int tend = t0 < t1 ? min(len, t1 + K - 1) : t0;
+    auto fetch = [&](int t, int slot) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-#pragma unroll
-            for (int k = 0; k + 1 < K; ++k) { xs[e][k] = xs[e][k + 1]; gs[e][k] = gs[e][k + 1]; }
-            xs[e][K - 1] = to_f(rx.v[e]);
-            float g = to_f(rg.v[e]);
-            if (a.silu) {
-                float p = bias[e];
-#pragma unroll
-                for (int k = 0; k < K; ++k) p = fmaf(w[e][k], xs[e][k], p);
-                g *= dsilu_f<T>(p);
+        for (int i = 0; i < U; ++i) {
+            const bool ok = t + i < tend;
+            const size_t at = ok ? (size_t)(t + i) * D : 0;
+            if constexpr (V > 1) {
+                copy_async(&ring[slot][0][i][threadIdx.x], x + at, ok);
+                copy_async(&ring[slot][1][i][threadIdx.x], dout + at, ok);
+            } else {
+                ahead[0][i] = ok ? load_pack<T, V>(x + at) : zero_pack<T, V>();
+                ahead[1][i] = ok ? load_pack<T, V>(dout + at) : zero_pack<T, V>();
             }
-            if (!in) g = 0.f;
-            gs[e][K - 1] = g;
-            if (own) {
-                db[e] += g;
-#pragma unroll
-                for (int k = 0; k < K; ++k) dw[e][k] = fmaf(g, xs[e][k], dw[e][k]);
-            }
-            // dx of token t-K+1: taps k meet g[t-K+1 + K-1-k] = gs[K-1-k]
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) s = fmaf(w[e][k], gs[e][K - 1 - k], s);
-            from_f(o.v[e], s);
         }
-        if (t - (K - 1) >= t0) *reinterpret_cast<Pack<T, V>*>(dx + (size_t)(t - (K - 1)) * D) = o;
+        if constexpr (V > 1) copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < (V > 1 ? STAGES - 1 : 1); ++s) fetch(t0 + s * U, s);
+    int slot = 0;
+    for (int t4 = t0; t4 < t1 + K - 1 && t0 < t1; t4 += U) {
+        Pack<T, V> rx[U], rg[U];
+        if constexpr (V > 1) copy_wait<STAGES - 2>();
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if constexpr (V > 1) {
+                rx[i] = ring[slot][0][i][threadIdx.x];
+                rg[i] = ring[slot][1][i][threadIdx.x];
+            } else {
+                rx[i] = ahead[0][i];
+                rg[i] = ahead[1][i];
+            }
+        }
+        if constexpr (V > 1) fetch(t4 + (STAGES - 1) * U, slot ? slot - 1 : STAGES - 1);
+        else fetch(t4 + U, 0);
+        slot = slot + 1 < STAGES ? slot + 1 : 0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = t4 + i;
+            const bool in = t < len, own = t < t1;
+            Pack<T, V> o;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+#pragma unroll
+                for (int k = 0; k + 1 < K; ++k) { xs[e][k] = xs[e][k + 1]; gs[e][k] = gs[e][k + 1]; }
+                xs[e][K - 1] = to_f(rx[i].v[e]);
+                float g = to_f(rg[i].v[e]);
+                if (a.silu) {
+                    float p = bias[e];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) p = fmaf(w[e][k], xs[e][k], p);
+                    g *= dsilu_f<T>(p);
+                }
+                if (!in) g = 0.f;
+                gs[e][K - 1] = g;
+                if (own) {
+                    db[e] += g;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) dw[e][k] = fmaf(g, xs[e][k], dw[e][k]);
+                }
+                // dx of token t-K+1: taps k meet g[t-K+1 + K-1-k] = gs[K-1-k]
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) s = fmaf(w[e][k], gs[e][K - 1 - k], s);
+                from_f(o.v[e], s);
+            }
+            if (t - (K - 1) >= t0 && t - (K - 1) < t1)
+                *reinterpret_cast<Pack<T, V>*>(dx + (size_t)(t - (K - 1)) * D) = o;
+        }
     }
+    if constexpr (V > 1) copy_wait<0>();
     float* row = part + (size_t)(b * runs + run) * D * (K + 1) + (size_t)c;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -225,6 +315,7 @@ __global__ void __launch_bounds__(256) k_conv_reduce(const float* part, int rows
     }
 }
 
+// Whether rows of 16-byte columns (and the parameters with them) start on 16 bytes.
 static bool vector_rows(const SsmHandle& h, std::initializer_list<const void*> ptrs) {
     const int v = h.dtype == FAVOR_DTYPE_F32 ? 4 : 8;
     if (h.D % v) return false;
@@ -252,13 +343,16 @@ static void conv_dispatch(const SsmHandle& h, bool vec, A... args) {
 
 static int conv_cblocks(int D, int V) { return (D + kConvThreads * V - 1) / (kConvThreads * V); }
 
-constexpr int kConvRun = 8;
-
 template <typename T, int V, int K>
 struct ConvPrompt {
     static void go(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
-        const int cb = conv_cblocks(h.D, V), runs = (a.L + kConvRun - 1) / kConvRun;
-        k_conv<T, V, K, kConvRun><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs);
+        constexpr int VP = V < 4 ? V : 4;
+        const int cb = conv_cblocks(h.D, VP);
+        // Runs of 64 tokens where they fill the SMs with 8 blocks each, down to 8 where they do not
+        int R = 64;
+        while (R > 8 && (long long)cb * a.B * ((a.L + R - 1) / R) < (long long)h.num_sms * 8) R /= 2;
+        const int runs = (a.L + R - 1) / R;
+        k_conv<T, VP, K><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs, R);
     }
 };
 
@@ -277,8 +371,9 @@ constexpr int kConvBwdRun = 64;
 template <typename T, int V, int K>
 struct ConvBwd {
     static void go(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
-        const int cb = conv_cblocks(h.D, V), runs = (a.L + kConvBwdRun - 1) / kConvBwdRun;
-        k_conv_bwd<T, V, K><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs, kConvBwdRun, h.ws);
+        constexpr int VB = V < 4 ? V : 4;   // the sums of 8 channels would take 144 registers
+        const int cb = conv_cblocks(h.D, VB), runs = (a.L + kConvBwdRun - 1) / kConvBwdRun;
+        k_conv_bwd<T, VB, K><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs, kConvBwdRun, h.ws);
         const int n = h.D * (K + 1);
         k_conv_reduce<<<(n + 31) / 32, 256, 0, st>>>(h.ws, a.B * runs, h.D, K, a.dweight, a.dbias);
     }
@@ -289,19 +384,19 @@ size_t conv_backward_ws(const SsmHandle& h) {
 }
 
 favor_status conv_prompt(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
-    conv_dispatch<ConvPrompt>(h, vector_rows(h, {a.x, a.out, a.window}), a, st);
+    conv_dispatch<ConvPrompt>(h, vector_rows(h, {a.x, a.out, a.window, a.weight, a.bias}), a, st);
     count_launch();
     return check_launch("favor_conv_causal");
 }
 
 favor_status conv_step(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
-    conv_dispatch<ConvStep>(h, vector_rows(h, {a.x, a.out, a.window}), a, st);
+    conv_dispatch<ConvStep>(h, vector_rows(h, {a.x, a.out, a.window, a.weight, a.bias}), a, st);
     count_launch();
     return check_launch("favor_conv_causal_step");
 }
 
 favor_status conv_backward(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
-    conv_dispatch<ConvBwd>(h, vector_rows(h, {a.x, a.dout, a.dx}), a, st);
+    conv_dispatch<ConvBwd>(h, vector_rows(h, {a.x, a.dout, a.dx, a.weight, a.bias}), a, st);
     count_launch(2);
     return check_launch("favor_conv_causal_backward");
 }

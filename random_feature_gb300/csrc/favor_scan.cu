@@ -127,7 +127,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 const bool ok = t + ev_t[v] < t1 && ev_c[v] * V < cn && (k < 2 || z);
                 const T* at = ok ? src[k] + (size_t)(t + ev_t[v]) * D + ev_c[v] * V : u;
                 if constexpr (V > 1) {
-                    copy16_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
+                    copy_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
                 } else {
                     rr[k][v] = ok ? load_pack<T, V>(at) : zero_pack<T, V>();
                 }
@@ -141,7 +141,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 const bool ok = e < BC && t + tt < t1;
                 const T* at = ok ? mat[k] + (size_t)(t + tt) * G * N + n : mat[k];
                 if constexpr (V > 1) {
-                    if (e < BC) copy16_async(&sm.rawbc[slot][k][i][threadIdx.x], at, ok);
+                    if (e < BC) copy_async(&sm.rawbc[slot][k][i][threadIdx.x], at, ok);
                 } else {
                     from_f(rbc[k][i], 0.f);
                     if (ok) rbc[k][i] = *at;
@@ -384,48 +384,92 @@ __global__ void __launch_bounds__(128) k_scan_chain(ScanArgs p, ScanPlan pl, Sca
     }
 }
 
-// One token a row: a thread holds 4 states (16 bytes) of a channel, N/4 lanes a
-// channel.  Bound by the state, read and written once.
+// One token a row.  A thread holds 4 states (16 bytes) of CH channels, LPC = N/4
+// lanes a channel; what is done once a channel (dt, the gate, the output) is done
+// by one lane each.  Bound by the state, read and written once: its loads are
+// issued before anything that waits.
 template <typename T, int N>
-__global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanArgs p, int D, int G, int cblocks) {
-    constexpr int LPC = N / 4;
-    const int cb = blockIdx.x % cblocks, b = blockIdx.x / cblocks;
-    const int i = cb * kScanThreads + threadIdx.x, c = i / LPC, part = i % LPC;
-    const bool in = c < D;
-    const int cc = in ? c : 0, g = cc / (D / G);
-    const float* A = p.A + (size_t)cc * N + part * 4;
-    const float a0 = A[0], a1 = A[1], a2 = A[2], a3 = A[3];
-    const T* Bm = (const T*)p.Bm + ((size_t)b * G + g) * N + part * 4;
-    const T* Cm = (const T*)p.Cm + ((size_t)b * G + g) * N + part * 4;
-    float bm[4], cm[4];
+__global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanArgs p, int D, int G, int cblocks, bool wide) {
+    constexpr int LPC = N / 4, CH = LPC < 4 ? LPC : 4, Q = kScanThreads / LPC;
+    const int cb = blockIdx.x % cblocks, b = blockIdx.x / cblocks, part = threadIdx.x % LPC, q = threadIdx.x / LPC;
+    const int c0 = cb * Q * CH + q, Dg = D / G;
+    // the lane's own channel: the index that the sums over lanes below leave with it
+    const int own = CH == 4 ? (part & 1) * 2 + (part >> 1 & 1) : part & 1;
+    int page = row_page(p.pg, b);
+    float* sp = p.state + ((size_t)(page < 0 ? 0 : page) * D + c0) * N + part * 4;
+    const float* A = p.A + (size_t)c0 * N + part * 4;
+    float4 h[CH], a[CH];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) { bm[k] = to_f(Bm[k]); cm[k] = to_f(Cm[k]); }
-    const size_t at = (size_t)b * D + cc;
+    for (int i = 0; i < CH; ++i) {
+        const bool in = c0 + i * Q < D;
+        h[i] = in ? *reinterpret_cast<const float4*>(sp + i * Q * N) : make_float4(0.f, 0.f, 0.f, 0.f);
+        a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in && wide) a[i] = *reinterpret_cast<const float4*>(A + i * Q * N);
+        if (in && !wide) a[i] = make_float4(A[i * Q * N], A[i * Q * N + 1], A[i * Q * N + 2], A[i * Q * N + 3]);
+    }
+    const int co = min(c0 + own * Q, D - 1);
+    const size_t at = (size_t)b * D + co;
     const float uu = to_f(((const T*)p.u)[at]);
-    const float raw = to_f(((const T*)p.dt)[at]) + (p.dt_bias ? p.dt_bias[cc] : 0.f);
+    const float raw = to_f(((const T*)p.dt)[at]) + (p.dt_bias ? p.dt_bias[co] : 0.f);
     const float zz = p.z ? to_f(((const T*)p.z)[at]) : 0.f;
-    const float sk = p.skip ? p.skip[cc] : 0.f;
-    const int page = block_page(p.pg, b);
+    const float sk = p.skip ? p.skip[co] : 0.f;
+    float bm[4], cm[4];
+    auto load_bc = [&](int c) {
+        const size_t bc = ((size_t)b * G + min(c, D - 1) / Dg) * N + part * 4;
+        if (wide) {
+            const Pack<T, 4> b4 = load_pack<T, 4>((const T*)p.Bm + bc), c4 = load_pack<T, 4>((const T*)p.Cm + bc);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bm[k] = to_f(b4.v[k]);
+                cm[k] = to_f(c4.v[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bm[k] = to_f(((const T*)p.Bm)[bc + k]);
+                cm[k] = to_f(((const T*)p.Cm)[bc + k]);
+            }
+        }
+    };
+    load_bc(c0);
+    if (block_page_taken(p.pg, b, page)) page = -1;
+    const bool mine = part < CH && c0 + own * Q < D;
     if (page < 0) {   // the row takes no part
-        if (in && part == 0) from_f(((T*)p.out)[at], 0.f);
+        if (mine) from_f(((T*)p.out)[at], 0.f);
         return;
     }
-    float4* sp = reinterpret_cast<float4*>(p.state + ((size_t)page * D + cc) * N + part * 4);
-    float4 h = *sp;
     const float d = softplus_f(raw), x = d * uu, dl = d * kLog2e;
-    h.x = fmaf(ex2_approx(fmaf(a0, dl, kEx2Mean)), h.x, x * bm[0]);
-    h.y = fmaf(ex2_approx(fmaf(a1, dl, kEx2Mean)), h.y, x * bm[1]);
-    h.z = fmaf(ex2_approx(fmaf(a2, dl, kEx2Mean)), h.z, x * bm[2]);
-    h.w = fmaf(ex2_approx(fmaf(a3, dl, kEx2Mean)), h.w, x * bm[3]);
-    if (in) *sp = h;
-    float y = fmaf(h.x, cm[0], h.y * cm[1]) + fmaf(h.z, cm[2], h.w * cm[3]);
+    float y[CH];
 #pragma unroll
-    for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (in && part == 0) {
-        y = fmaf(sk, uu, y);
-        if (p.z) y *= zz * sigmoid_f<T>(zz);
-        from_f(((T*)p.out)[at], y);
+    for (int i = 0; i < CH; ++i) {
+        if (i && G > 1) load_bc(c0 + i * Q);
+        // the lane of this channel's group that holds channel i
+        const int src = (threadIdx.x & 31 & ~(LPC - 1)) + (CH == 4 ? (i >> 1) + (i & 1) * 2 : i);
+        const float di = __shfl_sync(0xffffffffu, dl, src), xi = __shfl_sync(0xffffffffu, x, src);
+        h[i].x = fmaf(ex2_approx(fmaf(a[i].x, di, kEx2Mean)), h[i].x, xi * bm[0]);
+        h[i].y = fmaf(ex2_approx(fmaf(a[i].y, di, kEx2Mean)), h[i].y, xi * bm[1]);
+        h[i].z = fmaf(ex2_approx(fmaf(a[i].z, di, kEx2Mean)), h[i].z, xi * bm[2]);
+        h[i].w = fmaf(ex2_approx(fmaf(a[i].w, di, kEx2Mean)), h[i].w, xi * bm[3]);
+        if (c0 + i * Q < D) *reinterpret_cast<float4*>(sp + i * Q * N) = h[i];
+        y[i] = fmaf(h[i].x, cm[0], h[i].y * cm[1]) + fmaf(h[i].z, cm[2], h[i].w * cm[3]);
     }
+#pragma unroll
+    for (int o = 1, w = CH / 2; o < LPC; o <<= 1, w >>= 1) {
+        if (w) {
+            const bool up = part & o;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+                const float keep = up ? y[i + w] : y[i], give = up ? y[i] : y[i + w];
+                y[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        } else {
+            y[0] += __shfl_xor_sync(0xffffffffu, y[0], o);
+        }
+    }
+    if (!mine) return;
+    float v = fmaf(sk, uu, y[0]);
+    if (p.z) v *= zz * sigmoid_f<T>(zz);
+    from_f(((T*)p.out)[at], v);
 }
 
 // ------------------------------------------------------------------ launches
@@ -502,8 +546,9 @@ favor_status scan_prompt(const SsmHandle& h, const ScanArgs& a, cudaStream_t st)
 
 template <typename T, int N>
 static void step_launch(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
-    const int cb = (h.D * (N / 4) + kScanThreads - 1) / kScanThreads;
-    k_scan_step<T, N><<<(unsigned)cb * a.B, kScanThreads, 0, st>>>(a, h.D, h.G, cb);
+    const int per = kScanThreads / (N / 4) * (N / 4 < 4 ? N / 4 : 4), cb = (h.D + per - 1) / per;
+    k_scan_step<T, N><<<(unsigned)cb * a.B, kScanThreads, 0, st>>>(
+        a, h.D, h.G, cb, is_aligned16(a.A) && is_aligned16(a.Bm) && is_aligned16(a.Cm));
 }
 
 template <typename T>

@@ -104,12 +104,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 16 bytes global -> shared, asynchronously; zeros where !ok (src is not read then).
-__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "r"(ok ? 16 : 0)
-                 : "memory");
+// One pack (4, 8 or 16 bytes) global -> shared, asynchronously; zeros where !ok (src is not read then).
+template <typename P>
+__device__ __forceinline__ void copy_async(P* dst, const void* src, bool ok) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (sizeof(P) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(ok ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"((int)sizeof(P)),
+                     "r"(ok ? (int)sizeof(P) : 0)
+                     : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most N of this thread's committed groups are still in flight.
@@ -174,24 +178,39 @@ __device__ __forceinline__ float softplus_f(float x) {
 }
 
 // 1 / (1 + e^-x).  For 16-bit storage the approximate forms (relative error
-// below 2^-20) are far under the output's rounding of 2^-9; fp32 storage takes
-// the accurate ones.
+// below 2^-19 for |x| < 16) are far under the output's rounding of 2^-9.  fp32
+// storage adds what the product with log2 e lost to the exponent and one Newton step
+// to the reciprocal (e is kept finite for it; a NaN comes back through x itself
+// in every product this is used in).
 template <typename T>
 __device__ __forceinline__ float sigmoid_f(float x) {
-    if (sizeof(T) == 2) return rcp_approx(1.f + ex2_approx(-x * kLog2e));
-    return 1.f / (1.f + expf(-x));
+    const float t = -x * kLog2e;
+    float e = ex2_approx(t);
+    if (sizeof(T) == 2) return rcp_approx(1.f + e);
+    constexpr float lo = 1.925963033500e-8f;   // log2 e - kLog2e
+    const float r = fmaf(-x, lo, fmaf(-x, kLog2e, -t));
+    e = fminf(fmaf(e, r * 0.6931471805599453f, e), 1e38f);
+    const float d = 1.f + e, s = rcp_approx(d);
+    return fmaf(s, fmaf(-d, s, 1.f), s);
 }
 
-// Page of row b, or -1 if the row takes no part: a page outside the pool
-// (padding rows), or one that an earlier row of the call already names, so that
-// no page is written by two rows.  Every thread of the block gets the answer.
-__device__ __forceinline__ int block_page(const PageArgs& pg, int b) {
-    if (!pg.pages) return b < pg.n_pages ? b : -1;
-    const int page = pg.pages[b];
+// Page of row b, or -1 if it is outside the pool (padding rows).
+__device__ __forceinline__ int row_page(const PageArgs& pg, int b) {
+    const int page = pg.pages ? pg.pages[b] : b;
+    return page < 0 || page >= pg.n_pages ? -1 : page;
+}
+// Whether an earlier row of the call names row b's page too: such a row takes no
+// part, so that no page is written by two rows.  For every thread of the block.
+__device__ __forceinline__ bool block_page_taken(const PageArgs& pg, int b, int page) {
+    if (!pg.pages) return false;
     int dup = 0;
     for (int j = threadIdx.x; j < b; j += blockDim.x) dup |= pg.pages[j] == page;
-    dup = __syncthreads_or(dup);
-    return (page < 0 || page >= pg.n_pages || dup) ? -1 : page;
+    return __syncthreads_or(dup);
+}
+// Page of row b, or -1 if the row takes no part.
+__device__ __forceinline__ int block_page(const PageArgs& pg, int b) {
+    const int page = row_page(pg, b);
+    return block_page_taken(pg, b, page) ? -1 : page;
 }
 
 // Length of row b: lens[b] clamped to [0, L].

@@ -8,6 +8,7 @@ device, and nothing falls back to anything when the library is missing.
 from __future__ import annotations
 
 import ctypes
+from operator import attrgetter
 
 from .favor import DTYPE_CODES, _check, _ptr, _stream, lib
 
@@ -91,10 +92,20 @@ def favor_pages_move(pool, n_pages, page_bytes, page_map, stream=None) -> None:
            "favor_pages_move")
 
 
-def _want(t, shape, dtype, device, name):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {list(shape)} on {device}, "
-                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+def _raw_stream(stream, index):
+    """The stream's address; torch's current one on the device by default.  (Looked up without building
+    a stream object: a decoding step's host time is mostly such calls.)"""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_kind = attrgetter("shape", "dtype", "device")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 class Ssm:
@@ -110,31 +121,30 @@ class Ssm:
         self.handle = None
         self.handle = favor_ssm_create(D, N, G, K, dtype, max_B, max_L, training)
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self._t = torch.float32 if DTYPE_CODES.get(dtype, dtype) == DTYPE_CODES["f32"] else torch.bfloat16
+        self._f32, self._i32, self._lib = torch.float32, torch.int32, lib()
+
+        # what the parameters have to be: shape, dtype, device
+        f32 = torch.float32
+        self._dims = (D,)
+        self._weight, self._vec, self._A = (((D, K), f32, self.device), ((D,), f32, self.device),
+                                            ((D, N), f32, self.device))
 
     # ---- checks
-    def _seq(self, t, lead, name, optional=False):
-        if t is None and optional:
-            return
-        _want(t, (*lead, self.D), self._t, self.device, name)
+    def _check_all(self, items):
+        """Every tensor of (tensor or None, (shape, dtype, device), name)."""
+        for t, want, name in items:
+            if t is not None and (_kind(t) != want or not t.is_contiguous()):
+                raise ValueError(f"{name}: expected contiguous {want[1]} {list(want[0])} on {want[2]}, "
+                                 f"got {t.dtype} {list(t.shape)} on {t.device}")
 
-    def _par(self, t, shape, name, optional=True):
-        import torch
-        if t is None and optional:
-            return
-        _want(t, shape, torch.float32, self.device, name)
-
-    def _int(self, t, n, name):
-        import torch
-        if t is not None:
-            _want(t, (n,), torch.int32, self.device, name)
-
-    def _pool(self, pool, page, dtype, name):
-        """Number of pages of a pool (0: none given)."""
+    def _pool(self, pool, page, dtype):
+        """(number of pages, what the pool has to be)."""
         if pool is None:
-            return 0
-        _want(pool, (pool.shape[0], *page), dtype, self.device, name)
-        return pool.shape[0]
+            return 0, None
+        P = pool.shape[0] if pool.dim() else 0
+        return P, ((P, *page), dtype, self.device)
 
     @staticmethod
     def _lead(x, dims, name):
@@ -142,12 +152,12 @@ class Ssm:
             raise ValueError(f"{name}: expected {dims} dimensions, got {list(x.shape)}")
         return tuple(x.shape[:-1])
 
-    def _out(self, like, out, lens):
+    def _out(self, like, out, lens=None):
         """The output: rows behind a row's end are left as they are, so a new one starts at zero."""
-        import torch
         if out is None:
+            import torch
             return torch.empty_like(like) if lens is None else torch.zeros_like(like)
-        _want(out, like.shape, like.dtype, like.device, "out")
+        self._check_all(((out, _kind(like), "out"),))
         return out
 
     # ---- states
@@ -162,99 +172,102 @@ class Ssm:
         return torch.zeros((P, self.K - 1, self.D), dtype=self._t, device=self.device)
 
     # ---- convolution
+    def _conv_args(self, lead, x, weight, bias, window, pages, lens):
+        """Checks; the number of window pages."""
+        P, pool = self._pool(window, (self.K - 1, self.D), self._t)
+        rows = (lead[:1], self._i32, self.device)
+        self._check_all(((x, (lead + self._dims, self._t, self.device), "x"), (weight, self._weight, "weight"),
+                         (bias, self._vec, "bias"), (window, pool, "window"), (pages, rows, "pages"),
+                         (lens, rows, "lens")))
+        return P
+
     def conv(self, x, weight, bias=None, silu=True, window=None, pages=None, lens=None, out=None, stream=None):
         """The convolution of x [B, L, D]; with window (pages [P, K-1, D]) it continues each row's
         past and keeps the row's last inputs."""
-        lead = self._lead(x, 3, "x")
-        self._seq(x, lead, "x")
-        self._par(weight, (self.D, self.K), "weight", optional=False)
-        self._par(bias, (self.D,), "bias")
-        P = self._pool(window, (self.K - 1, self.D), self._t, "window")
-        self._int(pages, lead[0], "pages")
-        self._int(lens, lead[0], "lens")
+        B, L = lead = self._lead(x, 3, "x")
+        P = self._conv_args(lead, x, weight, bias, window, pages, lens)
         out = self._out(x, out, lens)
-        favor_conv_causal(self.handle, x, weight, bias, silu, window, pages, P, lens, out, *lead, stream)
+        _check(self._lib.favor_conv_causal(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
+                                           _at(window), _at(pages), P, _at(lens), out.data_ptr(), B, L,
+                                           _raw_stream(stream, self._index)), "favor_conv_causal")
         return out
 
     def conv_step(self, x, weight, window, bias=None, silu=True, pages=None, out=None, stream=None):
         """One token a row, x [B, D]; the rows' windows move on."""
         lead = self._lead(x, 2, "x")
-        self._seq(x, lead, "x")
-        self._par(weight, (self.D, self.K), "weight", optional=False)
-        self._par(bias, (self.D,), "bias")
-        P = self._pool(window, (self.K - 1, self.D), self._t, "window")
-        self._int(pages, lead[0], "pages")
-        out = self._out(x, out, None)
-        favor_conv_causal_step(self.handle, x, weight, bias, silu, window, pages, P, out, *lead, stream)
+        P = self._conv_args(lead, x, weight, bias, window, pages, None)
+        out = self._out(x, out)
+        _check(self._lib.favor_conv_causal_step(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
+                                                _at(window), _at(pages), P, out.data_ptr(), lead[0],
+                                                _raw_stream(stream, self._index)), "favor_conv_causal_step")
         return out
 
     def conv_backward(self, x, weight, dout, bias=None, silu=True, lens=None, stream=None):
         """(dx, dweight, dbias) of conv(x, weight, bias, silu, lens=lens); dbias is None without bias."""
         import torch
-        lead = self._lead(x, 3, "x")
-        self._seq(x, lead, "x")
-        self._seq(dout, lead, "dout")
-        self._par(weight, (self.D, self.K), "weight", optional=False)
-        self._par(bias, (self.D,), "bias")
-        self._int(lens, lead[0], "lens")
+        B, L = lead = self._lead(x, 3, "x")
+        self._conv_args(lead, x, weight, bias, None, None, lens)
+        self._check_all(((dout, _kind(x), "dout"),))
         dx = self._out(x, None, lens)
         dweight = torch.empty_like(weight)
         dbias = None if bias is None else torch.empty_like(bias)
-        favor_conv_causal_backward(self.handle, x, weight, bias, silu, lens, dout, dx, dweight, dbias, *lead, stream)
+        _check(self._lib.favor_conv_causal_backward(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
+                                                    _at(lens), dout.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
+                                                    _at(dbias), B, L, _raw_stream(stream, self._index)),
+               "favor_conv_causal_backward")
         return dx, dweight, dbias
 
     # ---- scan
-    def _scan_args(self, lead, u, dt, A, Bm, Cm, skip, z, dt_bias):
-        self._seq(u, lead, "u")
-        self._seq(dt, lead, "dt")
-        self._seq(z, lead, "z", optional=True)
-        for t, name in ((Bm, "Bm"), (Cm, "Cm")):
-            _want(t, (*lead, self.G, self.N), self._t, self.device, name)
-        self._par(A, (self.D, self.N), "A", optional=False)
-        self._par(skip, (self.D,), "skip")
-        self._par(dt_bias, (self.D,), "dt_bias")
+    def _scan_args(self, lead, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, lens):
+        """Checks; the number of state pages."""
+        dev = self.device
+        P, pool = self._pool(state, (self.D, self.N), self._f32)
+        seq, mat = (lead + self._dims, self._t, dev), (lead + (self.G, self.N), self._t, dev)
+        rows = (lead[:1], self._i32, dev)
+        self._check_all(((u, seq, "u"), (dt, seq, "dt"), (z, seq, "z"), (Bm, mat, "Bm"), (Cm, mat, "Cm"),
+                         (A, self._A, "A"), (skip, self._vec, "skip"), (dt_bias, self._vec, "dt_bias"),
+                         (state, pool, "state"), (pages, rows, "pages"), (lens, rows, "lens")))
+        return P
 
     def scan(self, u, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, state=None, pages=None, lens=None, out=None,
              stream=None):
         """The scan of u, dt [B, L, D]; with state (pages [P, D, N]) it continues each row's past and
         leaves the state behind the row's last token."""
-        lead = self._lead(u, 3, "u")
-        self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias)
-        P = self._state(state)
-        self._int(pages, lead[0], "pages")
-        self._int(lens, lead[0], "lens")
+        B, L = lead = self._lead(u, 3, "u")
+        P = self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, lens)
         out = self._out(u, out, lens)
-        favor_ssm_scan(self.handle, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, P, lens, out, *lead, stream)
+        _check(self._lib.favor_ssm_scan(self.handle, u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                                        Cm.data_ptr(), _at(skip), _at(z), _at(dt_bias), _at(state), _at(pages), P,
+                                        _at(lens), out.data_ptr(), B, L, _raw_stream(stream, self._index)),
+               "favor_ssm_scan")
         return out
-
-    def _state(self, state):
-        import torch
-        return self._pool(state, (self.D, self.N), torch.float32, "state")
 
     def scan_step(self, u, dt, A, Bm, Cm, state, skip=None, z=None, dt_bias=None, pages=None, out=None, stream=None):
         """One token a row: u, dt [B, D], Bm, Cm [B, G, N]; the rows' states move on."""
         lead = self._lead(u, 2, "u")
-        self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias)
-        P = self._state(state)
-        self._int(pages, lead[0], "pages")
-        out = self._out(u, out, None)
-        favor_ssm_scan_step(self.handle, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, P, out, *lead, stream)
+        P = self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, None)
+        out = self._out(u, out)
+        _check(self._lib.favor_ssm_scan_step(self.handle, u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                                             Cm.data_ptr(), _at(skip), _at(z), _at(dt_bias), _at(state), _at(pages),
+                                             P, out.data_ptr(), lead[0], _raw_stream(stream, self._index)),
+               "favor_ssm_scan_step")
         return out
 
     def scan_backward(self, u, dt, A, Bm, Cm, dout, skip=None, z=None, dt_bias=None, lens=None, stream=None):
         """Gradients of scan(u, dt, A, Bm, Cm, skip, z, dt_bias, lens=lens) for the upstream gradient
         dout, as a dict: du, ddt, dA, dB, dC, dskip, dz, ddt_bias (None where the input is None)."""
         import torch
-        lead = self._lead(u, 3, "u")
-        self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias)
-        self._seq(dout, lead, "dout")
-        self._int(lens, lead[0], "lens")
+        B, L = lead = self._lead(u, 3, "u")
+        self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, None, None, lens)
+        self._check_all(((dout, _kind(u), "dout"),))
         new = torch.empty_like if lens is None else torch.zeros_like
         gr = dict(du=new(u), ddt=new(dt), dA=torch.empty_like(A), dB=new(Bm), dC=new(Cm),
                   dskip=None if skip is None else torch.empty_like(skip), dz=None if z is None else new(z),
                   ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias))
-        favor_ssm_scan_backward(self.handle, u, dt, A, Bm, Cm, skip, z, dt_bias, lens, dout, gr["du"], gr["ddt"],
-                                gr["dA"], gr["dB"], gr["dC"], gr["dskip"], gr["dz"], gr["ddt_bias"], *lead, stream)
+        _check(self._lib.favor_ssm_scan_backward(self.handle, u.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                                                 Bm.data_ptr(), Cm.data_ptr(), _at(skip), _at(z), _at(dt_bias),
+                                                 _at(lens), dout.data_ptr(), *(_at(g) for g in gr.values()), B, L,
+                                                 _raw_stream(stream, self._index)), "favor_ssm_scan_backward")
         return gr
 
     def close(self):
@@ -276,20 +289,26 @@ class Ssm:
 
 
 def _page_bytes(pool, name):
-    if pool.dim() < 1 or pool.numel() == 0 or not pool.is_cuda or not pool.is_contiguous():
+    n = pool.numel()
+    if n == 0 or pool.dim() < 1 or not pool.is_cuda or not pool.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous, non-empty CUDA tensor [pages, ...]")
-    return pool[0].numel() * pool.element_size()
+    return n // pool.shape[0] * pool.element_size()
 
 
-def _indices(t, device, name):
+def _indices(t, index, name):
     import torch
-    if t.dim() != 1 or t.numel() == 0 or t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous, non-empty int32 vector on {device}")
+    if t.dim() != 1 or t.numel() == 0 or t.dtype is not torch.int32 or t.get_device() != index \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous, non-empty int32 vector on cuda:{index}")
 
 
-def _on(pool):
+def _on(index, call):
+    """call() with the device current."""
     import torch
-    return torch.cuda.device(pool.device)
+    if torch._C._cuda_getDevice() == index:
+        return call()
+    with torch.cuda.device(index):
+        return call()
 
 
 def pages_copy(dst_pool, src_pool, src, dst, stream=None):
@@ -297,27 +316,30 @@ def pages_copy(dst_pool, src_pool, src, dst, stream=None):
     several times is forked).  Returns int32 [n]: 1 for a pair carried out, 0 for one left out (a
     page outside its pool, a destination named before, or, in one pool, one that the call reads)."""
     import torch
-    pb = _page_bytes(dst_pool, "dst_pool")
-    if _page_bytes(src_pool, "src_pool") != pb or src_pool.dtype != dst_pool.dtype \
-            or src_pool.device != dst_pool.device:
+    pb, index = _page_bytes(dst_pool, "dst_pool"), dst_pool.get_device()
+    if src_pool is not dst_pool and (_page_bytes(src_pool, "src_pool") != pb or src_pool.dtype is not dst_pool.dtype
+                                     or src_pool.get_device() != index):
         raise ValueError("the pools' pages differ in size, dtype or device")
-    _indices(src, dst_pool.device, "src")
-    _indices(dst, dst_pool.device, "dst")
-    if src.numel() != dst.numel():
-        raise ValueError(f"src names {src.numel()} pages and dst {dst.numel()}")
+    _indices(src, index, "src")
+    _indices(dst, index, "dst")
+    n = src.shape[0]
+    if n != dst.shape[0]:
+        raise ValueError(f"src names {n} pages and dst {dst.shape[0]}")
     done = torch.empty_like(src)
-    with _on(dst_pool):
-        favor_pages_copy(dst_pool, dst_pool.shape[0], src_pool, src_pool.shape[0], pb, src, dst, src.numel(), done,
-                         stream)
+    _check(_on(index, lambda: lib().favor_pages_copy(dst_pool.data_ptr(), dst_pool.shape[0], src_pool.data_ptr(),
+                                                     src_pool.shape[0], pb, src.data_ptr(), dst.data_ptr(), n,
+                                                     done.data_ptr(), _raw_stream(stream, index))),
+           "favor_pages_copy")
     return done
 
 
 def pages_clear(pool, pages, stream=None):
     """The named pages become the empty state (zeros); entries outside the pool are passed over."""
-    pb = _page_bytes(pool, "pool")
-    _indices(pages, pool.device, "pages")
-    with _on(pool):
-        favor_pages_clear(pool, pool.shape[0], pb, pages, pages.numel(), stream)
+    pb, index = _page_bytes(pool, "pool"), pool.get_device()
+    _indices(pages, index, "pages")
+    _check(_on(index, lambda: lib().favor_pages_clear(pool.data_ptr(), pool.shape[0], pb, pages.data_ptr(),
+                                                      pages.shape[0], _raw_stream(stream, index))),
+           "favor_pages_clear")
 
 
 def pages_compact(pool, table, others=(), stream=None):
@@ -325,20 +347,26 @@ def pages_compact(pool, table, others=(), stream=None):
     ``others`` (pools of one cache share the table).  Returns (new_table, n_live): where each entry's
     page is now (-1 for an entry that names none), and the number of live pages, int32 [1]."""
     import torch
-    pb = _page_bytes(pool, "pool")
-    _indices(table, pool.device, "table")
+    pb, index, P = _page_bytes(pool, "pool"), pool.get_device(), pool.shape[0]
+    _indices(table, index, "table")
     sizes = []
     for i, o in enumerate(others):
         sizes.append(_page_bytes(o, f"others[{i}]"))
-        if o.shape[0] != pool.shape[0] or o.device != pool.device:
-            raise ValueError(f"others[{i}]: expected {pool.shape[0]} pages on {pool.device}")
+        if o.shape[0] != P or o.get_device() != index:
+            raise ValueError(f"others[{i}]: expected {P} pages on cuda:{index}")
     new_table = torch.empty_like(table)
-    n_live = torch.empty(1, dtype=torch.int32, device=pool.device)
-    page_map = torch.empty(pool.shape[0], dtype=torch.int32, device=pool.device) if sizes else None
-    with _on(pool):
-        favor_pages_compact(pool, pool.shape[0], pb, table, table.numel(), new_table, page_map, n_live, stream)
+    n_live = table.new_empty(1)
+    page_map = table.new_empty(P) if sizes else None
+
+    def call():
+        s = _raw_stream(stream, index)
+        _check(lib().favor_pages_compact(pool.data_ptr(), P, pb, table.data_ptr(), table.shape[0],
+                                         new_table.data_ptr(), _at(page_map), n_live.data_ptr(), s),
+               "favor_pages_compact")
         for o, ob in zip(others, sizes):
-            favor_pages_move(o, o.shape[0], ob, page_map, stream)
+            _check(lib().favor_pages_move(o.data_ptr(), P, ob, page_map.data_ptr(), s), "favor_pages_move")
+
+    _on(index, call)
     return new_table, n_live
 
 
