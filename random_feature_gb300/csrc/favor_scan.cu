@@ -4,6 +4,7 @@
 //     y = sum_n C_n h_n + skip u,    out = y silu(z)
 // u, raw, z, out are [B, L, D]; B and C [B, L, G, N], group g serving the channels
 // g D/G .. (g+1) D/G - 1.  States and every sum are fp32.
+#include <initializer_list>
 #include <type_traits>
 
 #include "ssm_internal.h"
@@ -11,6 +12,7 @@
 namespace favor {
 
 constexpr int kScanThreads = 128;
+enum { SCAN_OUT, SCAN_SUM, SCAN_GRAD };
 
 // How a launch cuts channels and tokens.  A block is 128 threads over CPB
 // channels of one group of one row, for one chunk of tokens walked in tiles of
@@ -36,18 +38,13 @@ struct ScanPlan {
     int nC, Lc;    // chunks, tokens a chunk
 };
 
-// Chunk summaries in the workspace: for chunk j, the state it would end with from
-// an empty start, and the sum of its dt (whose exponential decays the start).
-struct ScanWs {
-    float* hend;   // [B][nC][D][N]
-    float* sdt;    // [B][nC][D]
-    float* h0;     // [B][D][N] the rows' own starts (the last chunk writes the page that they came from)
-};
-
-// SUMMARY: the first pass of a call with several chunks, every chunk but the last
-// of a row from an empty state, without C, z or outputs.  Otherwise the pass that
-// writes the outputs; k_scan_chain has turned the summaries' ends into the ends
-// of the whole row up to each chunk.
+// MODE: SCAN_OUT writes the outputs.  Where a row has several chunks they start
+// from ws.hs, which k_scan_chain has formed from the chunks' summaries: SCAN_SUM
+// leaves there the state that a chunk (all but a row's last) would end with from
+// an empty start, and the sum of its dt, whose exponential decays what came before.
+// SCAN_GRAD is the same for the backward call, over every chunk, with what the
+// chunk hands to the one before it when nothing is handed to it: with g the
+// gradient of y and P_t the product of a up to token t, sum_t P_t C_t g_t.
 //
 // A tile passes through three steps: every thread turns 8 elements (token,
 // channel) into dt and dt u in shared memory; the state lanes walk the tile's
@@ -59,26 +56,29 @@ struct ScanWs {
 // that the V channels of a thread's access land V different rows' width apart
 // and neighbouring threads write neighbouring words; the state lanes take the
 // places in order.
-template <typename T, int N, int V, bool SUMMARY>
+template <typename T, int N, int V, int MODE>
 struct ScanShared {
     static constexpr int LPC = N / kScanNS, CPB = kScanThreads * kScanCH / LPC;
     static constexpr int EPT = V > 1 ? 32 / (int)sizeof(T) : 8;        // elements a thread, two copies of 16 bytes
     static constexpr int TT = EPT * kScanThreads / CPB, NV = EPT / V, CV = CPB / V;
-    static constexpr int NT = SUMMARY ? 2 : 3, NM = SUMMARY ? 1 : 2;   // element tensors; B (and C)
+    static constexpr int NT = MODE == SCAN_OUT ? 3 : MODE == SCAN_SUM ? 2 : 4;   // u, dt, z, dout
+    static constexpr int NM = MODE == SCAN_SUM ? 1 : 2;                // B, C
     static constexpr int BV = V > 1 ? 16 / (int)sizeof(T) : 1;         // elements of B and C a copy
     static constexpr int BC = TT * N / BV, EB = (BC + kScanThreads - 1) / kScanThreads;
     Pack<T, V> raw[2][NT][NV][kScanThreads];
     Pack<T, BV> rawbc[2][NM][EB][kScanThreads];
     static constexpr int PAD = CV < 32 ? (CV < 2 ? 2 : CV) : 0;   // the rows that one warp's element lanes touch start on other banks
     alignas(16) float2 sdt[TT][CPB + PAD];      // (dt, dt u), then (y, )
+    alignas(16) float sg[MODE == SCAN_GRAD ? TT : 1][CPB + PAD];
     alignas(16) float sbias[CV][V], sskip[CV][V];
     alignas(16) float bc[NM][TT][N];
 };
 
-template <typename T, int N, int V, bool SUMMARY>
+template <typename T, int N, int V, int MODE>
 __global__ void __launch_bounds__(kScanThreads, kScanPerSm)
 k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
-    using S = ScanShared<T, N, V, SUMMARY>;
+    using S = ScanShared<T, N, V, MODE>;
+    constexpr bool OUT = MODE == SCAN_OUT, GRAD = MODE == SCAN_GRAD;
     constexpr int LPC = S::LPC, CPB = S::CPB, TT = S::TT, NV = S::NV, CV = S::CV, BV = S::BV, BC = S::BC, EB = S::EB;
     constexpr int NS = kScanNS, CH = kScanCH;
     constexpr int GK = LPC < 2 ? 1 : LPC / 2;   // tokens whose y are summed over the lanes together: LPC values
@@ -90,16 +90,17 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     const int b = rest % p.B, chunk = rest / p.B;
     const int len = row_len(p.lens, b, p.L);
     const int t0 = chunk * pl.Lc, t1 = min(t0 + pl.Lc, len);
-    if (t0 >= t1 || (SUMMARY && t1 == len)) return;
-    const int page = p.state ? block_page(p.pg, b) : 0;
+    if (t0 >= t1 || (MODE == SCAN_SUM && t1 == len)) return;
+    const int page = OUT && p.state ? block_page(p.pg, b) : 0;
     const int g = tile / pl.tpg, cl = (tile % pl.tpg) * CPB, c0 = g * pl.Dg + cl, cn = min(CPB, pl.Dg - cl);
     const size_t row = (size_t)b * p.L;
     const T* u = (const T*)p.u + row * D + c0;
     const T* dt = (const T*)p.dt + row * D + c0;
-    const T* z = p.z && !SUMMARY ? (const T*)p.z + row * D + c0 : nullptr;
-    T* out = (T*)p.out + row * D + c0;
+    const T* z = p.z && MODE != SCAN_SUM ? (const T*)p.z + row * D + c0 : nullptr;
+    const T* dout = GRAD ? (const T*)p.dout + row * D + c0 : nullptr;
+    T* out = OUT ? (T*)p.out + row * D + c0 : nullptr;
     if (page < 0) {   // the row takes no part
-        if (!SUMMARY)
+        if (OUT)
             for (int i = threadIdx.x; i < (t1 - t0) * cn; i += kScanThreads)
                 from_f(out[(size_t)(t0 + i / cn) * D + i % cn], 0.f);
         return;
@@ -119,12 +120,12 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     Pack<T, V> rr[V == 1 ? S::NT : 1][V == 1 ? NV : 1];
     T rbc[V == 1 ? S::NM : 1][V == 1 ? EB : 1];
     auto fetch = [&](int t, int slot) {
-        const T* src[3] = {u, dt, z};
+        const T* src[4] = {u, dt, z, dout};
 #pragma unroll
         for (int k = 0; k < S::NT; ++k)
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const bool ok = t + ev_t[v] < t1 && ev_c[v] * V < cn && (k < 2 || z);
+                const bool ok = t + ev_t[v] < t1 && ev_c[v] * V < cn && (k != 2 || z);
                 const T* at = ok ? src[k] + (size_t)(t + ev_t[v]) * D + ev_c[v] * V : u;
                 if constexpr (V > 1) {
                     copy_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
@@ -185,20 +186,21 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         }
     }
     uint64_t A2[CH][NS / 2], h[CH][NS / 2];
+    uint64_t P[GRAD ? CH : 1][NS / 2], mu[GRAD ? CH : 1][NS / 2];
     const uint64_t mean2 = pack2(kEx2Mean, kEx2Mean);
-    float* stp = p.state ? p.state + (size_t)page * D * N : nullptr;
-    float* h0p = ws.h0 + (size_t)b * D * N;
-    // The page's state: read here by the pass that does not write pages, unless chunk 0 is all of the row.
-    const float* start = SUMMARY || t1 == len ? stp : h0p;
-    if (chunk) start = SUMMARY ? nullptr : ws.hend + ((size_t)b * pl.nC + chunk - 1) * D * N;
-    else if (!stp) start = nullptr;
+    float* stp = OUT && p.state ? p.state + (size_t)page * D * N : nullptr;
+    // Several chunks: one of them writes the page while others start, so they start from the workspace.
+    const float* start = !OUT ? nullptr : pl.nC > 1 ? ws.hs + ((size_t)b * pl.nC + chunk) * D * N : stp;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int n = 0; n < NS / 2; ++n) {
             A2[c][n] = pack2(p.A[cn0[c] + 2 * n] * kLog2e, p.A[cn0[c] + 2 * n + 1] * kLog2e);
             h[c][n] = start ? *reinterpret_cast<const uint64_t*>(start + cn0[c] + 2 * n) : 0ull;
-            if (SUMMARY && start && live[c]) *reinterpret_cast<uint64_t*>(h0p + cn0[c] + 2 * n) = h[c][n];
+            if (GRAD) {
+                P[c][n] = pack2(1.f, 1.f);
+                mu[c][n] = 0ull;
+            }
         }
     float total_dt[CH] = {};
 
@@ -216,29 +218,40 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 const uint64_t d2 = pack2(dd[c], dd[c]);
 #pragma unroll
                 for (int n = 0; n < NS / 2; ++n) a[c][n] = ex2_2(fma2(A2[c][n], d2, mean2));
-                if (SUMMARY) total_dt[c] += dd[c];
+                if (!OUT) total_dt[c] += dd[c];
             }
             const ulonglong2* B2 = reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt + k][part * NS]);
             const ulonglong2* C2 = reinterpret_cast<const ulonglong2*>(&sm.bc[S::NM - 1][tt + k][part * NS]);
-            uint64_t y2[CH], x2[CH];
+            uint64_t y2[CH], x2[CH], g2[CH];
+            float2 gg;
+            if (GRAD) gg = *reinterpret_cast<const float2*>(&sm.sg[tt + k][q * CH]);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) x2[c] = pack2(xx[c], xx[c]);
+            for (int c = 0; c < CH; ++c) {
+                x2[c] = pack2(xx[c], xx[c]);
+                if (GRAD) g2[c] = c ? pack2(gg.y, gg.y) : pack2(gg.x, gg.x);
+            }
 #pragma unroll
             for (int n = 0; n < NS / 4; ++n) {
                 const ulonglong2 bb = B2[n];
                 ulonglong2 cc;
-                if (!SUMMARY) cc = C2[n];
+                if (MODE != SCAN_SUM) cc = C2[n];
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     h[c][2 * n] = fma2(a[c][2 * n], h[c][2 * n], mul2(x2[c], bb.x));
                     h[c][2 * n + 1] = fma2(a[c][2 * n + 1], h[c][2 * n + 1], mul2(x2[c], bb.y));
-                    if (!SUMMARY) {
+                    if (GRAD) {
+                        P[c][2 * n] = mul2(P[c][2 * n], a[c][2 * n]);
+                        P[c][2 * n + 1] = mul2(P[c][2 * n + 1], a[c][2 * n + 1]);
+                        mu[c][2 * n] = fma2(P[c][2 * n], mul2(g2[c], cc.x), mu[c][2 * n]);
+                        mu[c][2 * n + 1] = fma2(P[c][2 * n + 1], mul2(g2[c], cc.y), mu[c][2 * n + 1]);
+                    }
+                    if (OUT) {
                         y2[c] = n ? fma2(h[c][2 * n], cc.x, y2[c]) : mul2(h[c][2 * n], cc.x);
                         y2[c] = fma2(h[c][2 * n + 1], cc.y, y2[c]);
                     }
                 }
             }
-            if (!SUMMARY) {
+            if (OUT) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     float y0, y1;
@@ -298,6 +311,15 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 sm.sdt[ev_t[v]][e * CV + ev_c[v]] = make_float2(d[e], d[e] * to_f(ru.v[e]));
+            if constexpr (GRAD) {
+                const Pack<T, V> rz = sm.raw[slot][2][v][threadIdx.x], ro = sm.raw[slot][3][v][threadIdx.x];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float g = to_f(ro.v[e]);
+                    if (z) g *= to_f(rz.v[e]) * sigmoid_f<T>(to_f(rz.v[e]));
+                    sm.sg[ev_t[v]][e * CV + ev_c[v]] = g;
+                }
+            }
         }
 #pragma unroll
         for (int k = 0; k < S::NM; ++k)
@@ -317,7 +339,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         for (; tt + UN <= nt; tt += UN) {
             float y[UN * CH];
             tokens(tt, std::integral_constant<int, UN>(), y);
-            if (!SUMMARY) {
+            if (OUT) {
 #pragma unroll
                 for (int k = 0; k < UN; k += GK) finish(tt + k, y + k * CH, nt);
             }
@@ -327,10 +349,10 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
 #pragma unroll
             for (int k = 0; k < GK; ++k)
                 if (tt + k < nt) tokens(tt + k, std::integral_constant<int, 1>(), y + k * CH);
-            if (!SUMMARY) finish(tt, y, nt);
+            if (OUT) finish(tt, y, nt);
         }
         __syncthreads();
-        if (!SUMMARY) {
+        if constexpr (OUT) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 if (ev_t[v] >= nt || ev_c[v] * V >= cn) continue;
@@ -356,31 +378,62 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     for (int c = 0; c < CH; ++c) {
         if (!live[c]) continue;
         const size_t r = ((size_t)b * pl.nC + chunk) * D;
-        float* to = SUMMARY ? ws.hend + r * N : stp && t1 == len ? stp : nullptr;
+        float* to = !OUT ? ws.hs + r * N : stp && t1 == len ? stp : nullptr;
 #pragma unroll
-        for (int n = 0; n < NS / 2; ++n)
+        for (int n = 0; n < NS / 2; ++n) {
             if (to) *reinterpret_cast<uint64_t*>(to + cn0[c] + 2 * n) = h[c][n];
-        if (SUMMARY && part == 0) ws.sdt[r + c0 + ch[c]] = total_dt[c];
+            if (GRAD) *reinterpret_cast<uint64_t*>(ws.mu + r * N + cn0[c] + 2 * n) = mu[c][n];
+        }
+        if (!OUT && part == 0) ws.sdt[r + c0 + ch[c]] = total_dt[c];
     }
 }
 
-// Per (row, channel, state): h <- decay of the chunk h + the chunk's own end, in the
-// chunks' order (chunk 0's end holds the row's start already).
+// Per (row, channel, state), in the chunks' order: ws.hs from each chunk's own end to
+// its start, h <- decay of the chunk h + its own end, from the row's page (backward
+// call: from zero); there also ws.mu, the chunks' order reversed, from what each hands
+// on to what it is handed.  8 chunks' loads go ahead of the stores.
+template <bool GRAD>
 __global__ void __launch_bounds__(128) k_scan_chain(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int N) {
-    const size_t i = (size_t)blockIdx.x * 128 + threadIdx.x, DN = (size_t)D * N;
-    if (i >= (size_t)p.B * DN) return;
-    const int b = (int)(i / DN);
-    const size_t cn = i % DN;
-    const int c = (int)(cn / N), used = (row_len(p.lens, b, p.L) + pl.Lc - 1) / pl.Lc;   // the last one gave no summary
-    const float A = p.A[cn] * kLog2e;
-    float* hend = ws.hend + (size_t)b * pl.nC * DN + cn;
-    const float* sdt = ws.sdt + (size_t)b * pl.nC * D + c;
-    if (used < 2) return;
-    float h = hend[0];
-#pragma unroll 8
-    for (int j = 1; j < used - 1; ++j) {
-        h = fmaf(ex2_approx(A * sdt[(size_t)j * D]), h, hend[(size_t)j * DN]);
-        hend[(size_t)j * DN] = h;
+    const int DN = D * N, nb = (DN + 127) / 128, b = blockIdx.x / nb, i = blockIdx.x % nb * 128 + threadIdx.x, c = i / N;
+    const int page = !GRAD && p.state ? block_page(p.pg, b) : 0;
+    const int used = (row_len(p.lens, b, p.L) + pl.Lc - 1) / pl.Lc;
+    if (page < 0 || i >= DN) return;
+    const float A = p.A[i] * kLog2e;
+    const size_t r = (size_t)b * pl.nC;
+    const float* sdt = ws.sdt + r * D + c;
+    float h = !GRAD && p.state ? p.state[(size_t)page * DN + i] : 0.f, mu = 0.f;
+    float* hs = ws.hs + r * DN + i;
+    for (int j0 = 0; j0 < used; j0 += 8) {
+        float e[8], s[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool in = j0 + k < used - 1;   // the last one's own end is not asked for
+            e[k] = in ? hs[(size_t)(j0 + k) * DN] : 0.f;
+            s[k] = in ? sdt[(size_t)(j0 + k) * D] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (j0 + k >= used) break;
+            hs[(size_t)(j0 + k) * DN] = h;
+            h = fmaf(ex2_approx(A * s[k]), h, e[k]);
+        }
+    }
+    if (!GRAD) return;
+    float* ms = ws.mu + r * DN + i;
+    for (int j0 = used - 1; j0 >= 0; j0 -= 8) {
+        float e[8], s[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool in = j0 - k > 0;   // the first one hands to nobody
+            e[k] = in ? ms[(size_t)(j0 - k) * DN] : 0.f;
+            s[k] = in ? sdt[(size_t)(j0 - k) * D] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (j0 - k < 0) break;
+            ms[(size_t)(j0 - k) * DN] = mu;
+            mu = fmaf(ex2_approx(A * s[k]), mu, e[k]);
+        }
     }
 }
 
@@ -497,17 +550,14 @@ static ScanPlan scan_plan(const SsmHandle& h, int B, int L, int CPB, int TT) {
 // Several chunks come only while tiles * B * chunks <= SMs * kScanPerSm; a tile has
 // 128 * 16 states and at most 256 channels.
 size_t scan_prompt_ws(const SsmHandle& h) {
-    return (size_t)h.num_sms * kScanPerSm * (2 * kScanThreads * kScanNS * kScanCH + 256);
+    return (size_t)h.num_sms * kScanPerSm * (kScanThreads * kScanNS * kScanCH + 256);
 }
 
 template <typename T, int N, int V>
 static void scan_launch(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
-    using S = ScanShared<T, N, V, false>;
+    using S = ScanShared<T, N, V, SCAN_OUT>;
     const ScanPlan pl = scan_plan(h, a.B, a.L, S::CPB, S::TT);
-    ScanWs ws;
-    ws.hend = h.ws;
-    ws.h0 = ws.hend + (size_t)a.B * pl.nC * h.D * N;
-    ws.sdt = ws.h0 + (size_t)a.B * h.D * N;
+    const ScanWs ws = {h.ws, h.ws + (size_t)a.B * pl.nC * h.D * N, nullptr};
     auto launch = [&](auto kernel, size_t smem, int chunks) {
         // the attribute's failure shows as the launch's
         if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -515,12 +565,53 @@ static void scan_launch(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) 
         count_launch();
     };
     if (pl.nC > 1) {
-        launch(k_scan<T, N, V, true>, sizeof(ScanShared<T, N, V, true>), pl.nC - 1);
-        const size_t n = (size_t)a.B * h.D * N;
-        k_scan_chain<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(a, pl, ws, h.D, N);
+        launch(k_scan<T, N, V, SCAN_SUM>, sizeof(ScanShared<T, N, V, SCAN_SUM>), pl.nC - 1);
+        k_scan_chain<false><<<(unsigned)((h.D * N + 127) / 128) * a.B, 128, 0, st>>>(a, pl, ws, h.D, N);
         count_launch();
     }
-    launch(k_scan<T, N, V, false>, sizeof(ScanShared<T, N, V, false>), pl.nC);
+    launch(k_scan<T, N, V, SCAN_OUT>, sizeof(S), pl.nC);
+}
+
+// The chunk starts and incoming gradients of a backward call, into ws.hs and ws.mu.
+template <typename T, int N, int V>
+static void grad_launch(const SsmHandle& h, const ScanArgs& a, const ScanWs& ws, int Lc, cudaStream_t st) {
+    using S = ScanShared<T, N, V, SCAN_GRAD>;
+    ScanPlan pl;
+    pl.Dg = h.D / h.G;
+    pl.tpg = (pl.Dg + S::CPB - 1) / S::CPB;
+    pl.tiles = pl.tpg * h.G;
+    pl.Lc = Lc;
+    pl.nC = (a.L + Lc - 1) / Lc;
+    cudaFuncSetAttribute(k_scan<T, N, V, SCAN_GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S));
+    k_scan<T, N, V, SCAN_GRAD><<<(unsigned)pl.tiles * a.B * pl.nC, kScanThreads, sizeof(S), st>>>(a, pl, ws, h.D, h.G);
+    k_scan_chain<true><<<(unsigned)((h.D * N + 127) / 128) * a.B, 128, 0, st>>>(a, pl, ws, h.D, N);
+    count_launch(2);
+}
+
+template <typename T, int V>
+static void grad_by_n(const SsmHandle& h, const ScanArgs& a, const ScanWs& ws, int Lc, cudaStream_t st) {
+    if (h.N == 8) grad_launch<T, 8, V>(h, a, ws, Lc, st);
+    else if (h.N == 16) grad_launch<T, 16, V>(h, a, ws, Lc, st);
+    else if (h.N == 32) grad_launch<T, 32, V>(h, a, ws, Lc, st);
+    else grad_launch<T, 64, V>(h, a, ws, Lc, st);
+}
+
+// 16-byte accesses need every row of a group to start on one (rows of B and C are N >= 8 elements).
+static bool wide_rows(const SsmHandle& h, const ScanArgs& a) {
+    const int v = h.dtype == FAVOR_DTYPE_F32 ? 4 : 8;
+    for (const void* p : {a.u, a.dt, a.z, a.dout, a.Bm, a.Cm, (const void*)a.out, (const void*)a.du, (const void*)a.ddt,
+                          (const void*)a.dz})
+        if (!is_aligned16(p)) return false;
+    return h.D % v == 0 && (h.D / h.G) % v == 0;
+}
+
+bool scan_grad_chunks(const SsmHandle& h, const ScanArgs& a, const ScanWs& ws, int Lc, cudaStream_t st) {
+    const bool vec = wide_rows(h, a);
+    if (h.dtype == FAVOR_DTYPE_F32 && vec) grad_by_n<float, 4>(h, a, ws, Lc, st);
+    else if (h.dtype == FAVOR_DTYPE_F32) grad_by_n<float, 1>(h, a, ws, Lc, st);
+    else if (vec) grad_by_n<__nv_bfloat16, 8>(h, a, ws, Lc, st);
+    else grad_by_n<__nv_bfloat16, 1>(h, a, ws, Lc, st);
+    return vec;
 }
 
 template <typename T, int V>
@@ -533,10 +624,7 @@ static void scan_by_n(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
 
 favor_status scan_prompt(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
     const bool f32 = h.dtype == FAVOR_DTYPE_F32;
-    const int v = f32 ? 4 : 8;
-    // 16-byte accesses need every row of a group to start on one (rows of B and C are N >= 8 elements)
-    const bool vec = h.D % v == 0 && (h.D / h.G) % v == 0 && is_aligned16(a.u) && is_aligned16(a.dt) &&
-                     is_aligned16(a.z) && is_aligned16(a.out) && is_aligned16(a.Bm) && is_aligned16(a.Cm);
+    const bool vec = wide_rows(h, a);
     if (f32 && vec) scan_by_n<float, 4>(h, a, st);
     else if (f32) scan_by_n<float, 1>(h, a, st);
     else if (vec) scan_by_n<__nv_bfloat16, 8>(h, a, st);

@@ -7,59 +7,67 @@
 //     dA_n = sum_t dt q_n           dskip = sum_t g u,  ddt_bias = sum_t draw,  dz = dout y silu'(z)
 // The states are not kept by the forward call: they are formed again.
 //
-// Chunks of kBwdChunk tokens run in parallel.  k_bwd_summary gives each chunk's
-// end from an empty start, its decay (sum of dt), and what it hands to the
-// chunk before, a_first lambda_first from an empty end, as sum_t P_t C_t g_t with P_t
-// the running product of a; k_bwd_chain turns these into every chunk's start
-// state and incoming gradient; k_bwd_main walks a chunk forwards, keeping the
-// state at every 8th token, then backwards in tiles, where 8 tokens' states
-// and decays are held in registers.
+// Chunks of tokens run in parallel.  scan_grad_chunks leaves every chunk's start
+// state and the gradient that the chunk behind hands to it; k_bwd_main walks its
+// chunk forwards once, keeping the state at every 4th token in shared memory, then
+// backwards, 4 tokens at a time: their decays and states are formed again into
+// registers, and lambda runs back over them.
+#include <type_traits>
+
 #include "ssm_internal.h"
 
+#ifndef BCH
+#define BCH 64
+#define BMB 2
+#endif
 namespace favor {
 
 constexpr int kBwdThreads = 128;
-constexpr int kBwdChunk = 128;
-constexpr int kBwdSub = 8;          // tokens whose states are in registers at a time
+constexpr int kBwdSub = 4;          // tokens whose states are in registers at a time
 constexpr int kBwdTile = 16;        // tokens staged in shared memory at a time
-constexpr int kBwdNS = 4;           // states a thread
+constexpr int kBwdNS = 4;           // states a thread, of
+constexpr int kBwdCH = 2;           // channels
+// Tokens of a chunk: the kept states take 8 KB for every 4 of them.
+template <typename T> struct BwdChunk { static constexpr int value = sizeof(T) == 2 ? BCH : 32; };
 
 struct BwdPlan {
     int tiles, tpg, Dg, nC;
 };
 
 struct BwdWs {
-    float* hs;      // [B][nC][D][N] chunk ends, then chunk starts
-    float* mu;      // [B][nC][D][N] gradients handed back by a chunk, then handed to it
-    float* sdt;     // [B][nC][D]
+    ScanWs s;
     float* dA;      // [B][nC][D][N]
     float* dskip;   // [B][nC][D]
     float* dbias;   // [B][nC][D]
-    float* bc;      // [tpg][B][L][G][2N] per channel tile: dB, dC
+    float* bc;      // [tpg][B][L][G][N/4][2][4] per channel tile: dB, dC of 4 states
 };
 
 static BwdWs bwd_layout(float* ws, const BwdPlan& pl, int B, int L, int D, int N, int G, size_t* total) {
     BwdWs w;
     const size_t rows = (size_t)B * pl.nC;
     float* at = ws;
-    w.hs = at; at += rows * D * N;
-    w.mu = at; at += rows * D * N;
+    w.s.hs = at; at += rows * D * N;
+    w.s.mu = at; at += rows * D * N;
     w.dA = at; at += rows * D * N;
     w.bc = at; at += (size_t)pl.tpg * B * L * G * 2 * N;
-    w.sdt = at; at += rows * D;
+    w.s.sdt = at; at += rows * D;
     w.dskip = at; at += rows * D;
     w.dbias = at; at += rows * D;
     *total = (size_t)(at - ws);
     return w;
 }
 
+static int bwd_chunk(const SsmHandle& h) {
+    return h.dtype == FAVOR_DTYPE_F32 ? BwdChunk<float>::value : BwdChunk<__nv_bfloat16>::value;
+}
+
 static BwdPlan bwd_plan(const SsmHandle& h, int L) {
     BwdPlan pl;
-    const int CPB = kBwdThreads * kBwdNS / h.N;
+    const int CPB = kBwdThreads * kBwdNS * kBwdCH / h.N;
     pl.Dg = h.D / h.G;
     pl.tpg = (pl.Dg + CPB - 1) / CPB;
     pl.tiles = pl.tpg * h.G;
-    pl.nC = (L + kBwdChunk - 1) / kBwdChunk;
+    pl.nC = (L + bwd_chunk(h) - 1) / bwd_chunk(h);
     return pl;
 }
 
@@ -69,369 +77,416 @@ size_t scan_backward_ws(const SsmHandle& h) {
     return n;
 }
 
-// Elements (tokens x channels) of a staged tile, V channels an access.
-template <typename T, int N, int V, int TL>
-struct Elems {
-    static constexpr int CPB = kBwdThreads * kBwdNS / N;
-    static constexpr int CV = CPB / V;
-    static constexpr int NV = (TL * CPB / V + kBwdThreads - 1) / kBwdThreads;
-};
-
-template <typename T, int N, int V>
-__global__ void __launch_bounds__(kBwdThreads) k_bwd_summary(ScanArgs p, BwdPlan pl, BwdWs ws, int D, int G) {
-    using E = Elems<T, N, V, kBwdTile>;
-    constexpr int NS = kBwdNS, LPC = N / NS, CPB = E::CPB;
-    __shared__ float s_dt[kBwdTile][CPB], s_x[kBwdTile][CPB], s_g[kBwdTile][CPB];
-    __shared__ __align__(16) float sB[kBwdTile][N], sC[kBwdTile][N];
-    const int tile = blockIdx.x % pl.tiles, rest = blockIdx.x / pl.tiles;
-    const int b = rest % p.B, chunk = rest / p.B;
-    const int len = row_len(p.lens, b, p.L);
-    const int t0 = chunk * kBwdChunk, t1 = min(t0 + kBwdChunk, len);
-    if (t0 >= t1) return;
-    const int g = tile / pl.tpg, cl = (tile % pl.tpg) * CPB, c0 = g * pl.Dg + cl, cn = min(CPB, pl.Dg - cl);
-    const size_t row = (size_t)b * p.L;
-    const int ch = threadIdx.x / LPC, part = threadIdx.x % LPC;
-    const bool live = ch < cn;
-    const size_t cn0 = (size_t)(c0 + (live ? ch : 0)) * N + part * NS;
-    float A[NS], h[NS], mu[NS], P[NS], sum_dt = 0.f;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        A[n] = p.A[cn0 + n] * kLog2e;
-        h[n] = mu[n] = 0.f;
-        P[n] = 1.f;
-    }
-    for (int t = t0; t < t1; t += kBwdTile) {
-        const int nt = min(kBwdTile, t1 - t);
-#pragma unroll
-        for (int v = 0; v < E::NV; ++v) {
-            const int i = v * kBwdThreads + threadIdx.x, tt = i / E::CV, c = i % E::CV * V;
-            if (tt >= kBwdTile) continue;
-            const bool ok = tt < nt && c < cn;
-            const size_t at = (row + t + tt) * D + c0 + c;
-            const Pack<T, V> ru = ok ? load_pack<T, V>((const T*)p.u + at) : zero_pack<T, V>();
-            const Pack<T, V> rd = ok ? load_pack<T, V>((const T*)p.dt + at) : zero_pack<T, V>();
-            const Pack<T, V> ro = ok ? load_pack<T, V>((const T*)p.dout + at) : zero_pack<T, V>();
-            Pack<T, V> rz = zero_pack<T, V>();
-            if (ok && p.z) rz = load_pack<T, V>((const T*)p.z + at);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float bias = ok && p.dt_bias && c + e < cn ? p.dt_bias[c0 + c + e] : 0.f;
-                const float d = softplus_f(to_f(rd.v[e]) + bias);
-                float gg = to_f(ro.v[e]);
-                if (p.z) gg *= to_f(rz.v[e]) * sigmoid_f<T>(to_f(rz.v[e]));
-                s_dt[tt][c + e] = d;
-                s_x[tt][c + e] = d * to_f(ru.v[e]);
-                s_g[tt][c + e] = gg;
-            }
-        }
-        for (int i = threadIdx.x; i < kBwdTile * N; i += kBwdThreads) {
-            const int tt = i / N, n = i % N;
-            const size_t at = ((row + t + tt) * G + g) * N + n;
-            sB[tt][n] = tt < nt ? to_f(((const T*)p.Bm)[at]) : 0.f;
-            sC[tt][n] = tt < nt ? to_f(((const T*)p.Cm)[at]) : 0.f;
-        }
-        __syncthreads();
-        for (int tt = 0; tt < nt; ++tt) {
-            const float d = s_dt[tt][ch], x = s_x[tt][ch], gg = s_g[tt][ch];
-            sum_dt += d;
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const float a = ex2_approx(A[n] * d);
-                h[n] = fmaf(a, h[n], x * sB[tt][part * NS + n]);
-                P[n] *= a;
-                mu[n] = fmaf(P[n], gg * sC[tt][part * NS + n], mu[n]);
-            }
-        }
-        __syncthreads();
-    }
-    if (!live) return;
-    const size_t r = ((size_t)b * pl.nC + chunk) * D;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        ws.hs[r * N + cn0 + n] = h[n];
-        ws.mu[r * N + cn0 + n] = mu[n];
-    }
-    if (part == 0) ws.sdt[r + c0 + ch] = sum_dt;
-}
-
-// Per (row, channel, state): chunk ends -> chunk starts, forwards; what chunks hand
-// back -> what each is handed, backwards.
-__global__ void __launch_bounds__(256) k_bwd_chain(ScanArgs p, BwdPlan pl, BwdWs ws, int D, int N) {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, DN = (size_t)D * N;
-    if (i >= (size_t)p.B * DN) return;
-    const int b = (int)(i / DN);
-    const size_t cn = i % DN;
-    const int c = (int)(cn / N);
-    const int used = (row_len(p.lens, b, p.L) + kBwdChunk - 1) / kBwdChunk;
-    const float A = p.A[cn] * kLog2e;
-    const size_t r0 = (size_t)b * pl.nC;
-    float h = 0.f;
-#pragma unroll 8
-    for (int j = 0; j < used; ++j) {
-        float* at = ws.hs + (r0 + j) * DN + cn;
-        const float e = *at, s = ws.sdt[(r0 + j) * D + c];
-        *at = h;
-        h = fmaf(ex2_approx(A * s), h, e);
-    }
-    float mu = 0.f;
-#pragma unroll 8
-    for (int j = used - 1; j >= 0; --j) {
-        float* at = ws.mu + (r0 + j) * DN + cn;
-        const float e = *at, s = ws.sdt[(r0 + j) * D + c];
-        *at = mu;
-        mu = fmaf(ex2_approx(A * s), mu, e);
-    }
-}
-
-// Sums v[0..W) over the lanes that differ in the bits of lane at and above
-// `bit`: while more than one value is left each step halves the values a lane
-// holds (a lane with the bit set keeps the upper half), then plain butterflies.
-// On return v[0] (.. v[W / lanes)) of a lane holds its share.
-template <int W, int BIT>
+// Sums v[0..W) over the lanes that differ in the bits of lane at and above BIT:
+// while more than one value is left each step halves the values a lane holds (a
+// lane with the bit set keeps the upper half), then plain butterflies.  `first`
+// becomes the index of the lane's v[0].
+template <int W, int BIT, int END>
 struct LaneSum {
-    static __device__ __forceinline__ void go(float* v) {
-        if constexpr (BIT < 32) {
-            if constexpr (W > 1) {
+    static __device__ __forceinline__ void go(float* v, int& first) {
+        if constexpr (BIT < END) {
+            if constexpr (W % 2 == 0) {
                 const bool up = threadIdx.x & BIT;
 #pragma unroll
                 for (int i = 0; i < W / 2; ++i) {
                     const float keep = up ? v[i + W / 2] : v[i], give = up ? v[i] : v[i + W / 2];
                     v[i] = keep + __shfl_xor_sync(0xffffffffu, give, BIT);
                 }
-                LaneSum<W / 2, BIT * 2>::go(v);
+                first += up ? W / 2 : 0;
+                LaneSum<W / 2, BIT * 2, END>::go(v, first);
             } else {
-                v[0] += __shfl_xor_sync(0xffffffffu, v[0], BIT);
-                LaneSum<1, BIT * 2>::go(v);
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], BIT);
+                LaneSum<W, BIT * 2, END>::go(v, first);
             }
         }
     }
 };
+constexpr int lane_sum_left(int W, int lanes) { return lanes > 1 && W % 2 == 0 ? lane_sum_left(W / 2, lanes / 2) : W; }
 
 template <typename T, int N, int V>
-__global__ void __launch_bounds__(kBwdThreads) k_bwd_main(ScanArgs p, BwdPlan pl, BwdWs ws, int D, int G) {
-    using E = Elems<T, N, V, kBwdTile>;
-    constexpr int NS = kBwdNS, LPC = N / NS, CPB = E::CPB, CW = 32 / LPC, W = kBwdThreads / 32;
-    // values of dB | dC (4 + 4 a lane) left with a lane after the sum over its warp's channels
-    constexpr int LEFT = CW >= 8 ? 1 : 8 / CW;
+struct BwdShared {
+    static constexpr int LPC = N / kBwdNS, CPB = kBwdThreads * kBwdCH / LPC, PAIRS = CPB / 2, CV = CPB / V;
+    static constexpr int CHUNK = BwdChunk<T>::value, W = kBwdThreads / 32;
+    // Channel cl of a tile sits at place (cl % VP) (CPB / VP) + cl / VP of a shared row, as in the
+    // forward kernel; the narrow path keeps the places, and with them the order of the sums.
+    static constexpr int VP = 16 / (int)sizeof(T), PV = CPB / VP;
+    static __device__ __forceinline__ int place(int cl) { return cl % VP * PV + cl / VP; }
+    static constexpr int VECS = kBwdTile * CV, NV = (VECS + kBwdThreads - 1) / kBwdThreads;
+    static constexpr int BV = V > 1 ? 16 / (int)sizeof(T) : 1;
+    static constexpr int BC = kBwdTile * N / BV, EB = (BC + kBwdThreads - 1) / kBwdThreads;
+    static constexpr int PAD = 1;
+    float4 keep[CHUNK / kBwdSub][kBwdCH][kBwdThreads];
+    // a channel pair's (dt, dt u) twice and its g; then y twice, lambda B twice and A q
+    float4 dx[kBwdTile][PAIRS + PAD];
+    float2 g[kBwdTile][PAIRS + PAD];
+    alignas(16) float bc[2][kBwdTile][N];
+    alignas(16) float red[W][kBwdTile][LPC][8];
+    Pack<T, V> raw[2][4][NV][kBwdThreads];
+    Pack<T, BV> rawbc[2][2][EB][kBwdThreads];
+};
+
+template <typename T, int N, int V>
+__global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPlan pl, BwdWs ws, int D, int G) {
+    using S = BwdShared<T, N, V>;
+    constexpr int NS = kBwdNS, CH = kBwdCH, LPC = S::LPC, CPB = S::CPB, CV = S::CV, NV = S::NV, BV = S::BV, EB = S::EB;
+    constexpr int TL = kBwdTile, SUB = kBwdSub;
     extern __shared__ __align__(16) unsigned char smem[];
-    float4* keep = reinterpret_cast<float4*>(smem);                       // [chunk / sub][threads]
-    typedef float Row[CPB];
-    Row* s_dt = reinterpret_cast<Row*>(keep + (size_t)(kBwdChunk / kBwdSub) * kBwdThreads);   // [tile] -> lb
-    Row* s_u = s_dt + kBwdTile;                                           // -> sum A q
-    Row* s_g = s_u + kBwdTile;                                            // -> y
-    typedef float NRow[N];
-    NRow* sB = reinterpret_cast<NRow*>(s_g + kBwdTile);
-    NRow* sC = sB + kBwdTile;
-    float* red = reinterpret_cast<float*>(sC + kBwdTile);                 // [W][tile][2N]
+    S& sm = *reinterpret_cast<S*>(smem);
 
     const int tile = blockIdx.x % pl.tiles, rest = blockIdx.x / pl.tiles;
     const int b = rest % p.B, chunk = rest / p.B;
     const int len = row_len(p.lens, b, p.L);
-    const int t0 = chunk * kBwdChunk, t1 = min(t0 + kBwdChunk, len);
+    const int t0 = chunk * S::CHUNK, t1 = min(t0 + S::CHUNK, len);
     const int g = tile / pl.tpg, cl = (tile % pl.tpg) * CPB, c0 = g * pl.Dg + cl, cn = min(CPB, pl.Dg - cl);
     const size_t row = (size_t)b * p.L, wr = ((size_t)b * pl.nC + chunk) * D;
-    const int ch = threadIdx.x / LPC, part = threadIdx.x % LPC, warp = threadIdx.x / 32;
-    const bool live = ch < cn;
-    const size_t cn0 = (size_t)(c0 + (live ? ch : 0)) * N + part * NS;
-    if (t0 >= t1) {   // behind the row's end: nothing but zeros for the sums over rows
-        if (live) {
+    // state lanes: the channels at places 2q and 2q + 1 of the tile, states part*4 .. +3
+    const int q = threadIdx.x / LPC, part = threadIdx.x % LPC, warp = threadIdx.x / 32;
+    int ch[CH];
+    bool live[CH];
+    size_t cn0[CH];
 #pragma unroll
-            for (int n = 0; n < NS; ++n) ws.dA[wr * N + cn0 + n] = 0.f;
-            if (part == 0) ws.dskip[wr + c0 + ch] = ws.dbias[wr + c0 + ch] = 0.f;
+    for (int c = 0; c < CH; ++c) {
+        const int at = q * CH + c;
+        ch[c] = at % S::PV * S::VP + at / S::PV;
+        live[c] = ch[c] < cn;
+        if (!live[c]) ch[c] = 0;
+        cn0[c] = (size_t)(c0 + ch[c]) * N + part * NS;
+    }
+    if (t0 >= t1) {   // behind the row's end: zeros for the sums over rows
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (!live[c]) continue;
+            *reinterpret_cast<float4*>(ws.dA + wr * N + cn0[c]) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (part == 0) ws.dskip[wr + c0 + ch[c]] = ws.dbias[wr + c0 + ch[c]] = 0.f;
         }
         return;
     }
-    float A[NS], h[NS], mu[NS], dA[NS];
+    const T* src[4] = {(const T*)p.u, (const T*)p.dt, (const T*)p.z, (const T*)p.dout};
+    const T* mat[2] = {(const T*)p.Bm + (row * G + g) * N, (const T*)p.Cm + (row * G + g) * N};
+    Pack<T, V> rr[4][V == 1 ? NV : 1];
+    T rbc[2][V == 1 ? EB : 1];
+    // tile at t: nk = 2 tensors (forwards: u, dt, B) or 4 (backwards)
+    auto fetch = [&](int t, int slot, bool back) {
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        A[n] = p.A[cn0 + n] * kLog2e;
-        h[n] = ws.hs[wr * N + cn0 + n];
-        mu[n] = ws.mu[wr * N + cn0 + n];
-        dA[n] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+            if (k >= 2 && !back) break;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int i = v * kBwdThreads + threadIdx.x, tt = i / CV, c = i % CV * V;
+                const bool ok = i < S::VECS && t >= t0 && t + tt < t1 && c < cn && (k != 2 || p.z);
+                const T* at = ok ? src[k] + (row + t + tt) * D + c0 + c : src[0];
+                if constexpr (V > 1) copy_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
+                else rr[k][v] = ok ? load_pack<T, V>(at) : zero_pack<T, V>();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k && !back) break;
+#pragma unroll
+            for (int i = 0; i < EB; ++i) {
+                const int e = i * kBwdThreads + threadIdx.x, tt = e / (N / BV), n = e % (N / BV) * BV;
+                const bool ok = e < S::BC && t >= t0 && t + tt < t1;
+                const T* at = ok ? mat[k] + (size_t)(t + tt) * G * N + n : mat[k];
+                if constexpr (V > 1) {
+                    copy_async(&sm.rawbc[slot][k][i][threadIdx.x], at, ok);
+                } else {
+                    from_f(rbc[k][i], 0.f);
+                    if (ok) rbc[k][i] = *at;
+                }
+            }
+        }
+        if constexpr (V > 1) copy_commit();
+    };
+    auto bias_at = [&](const float* f, int c) { return f && c < cn ? f[c0 + c] : 0.f; };
+    // the tile's elements arrive: dt, dt u (and g) for the state lanes, B (and C)
+    auto arrive = [&](int slot, bool back) {
+        if constexpr (V > 1) {
+            copy_wait<1>();
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= 2 && !back) break;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) sm.raw[slot][k][v][threadIdx.x] = rr[k][v];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k && !back) break;
+#pragma unroll
+                for (int i = 0; i < EB; ++i) sm.rawbc[slot][k][i][threadIdx.x].v[0] = rbc[k][i];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * kBwdThreads + threadIdx.x, tt = i / CV, cv = i % CV;
+            if (i >= S::VECS) break;
+            const Pack<T, V> ru = sm.raw[slot][0][v][threadIdx.x], rd = sm.raw[slot][1][v][threadIdx.x];
+            float d[V + V % 2];
+            if constexpr (V == 1) d[1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] = to_f(rd.v[e]) + bias_at(p.dt_bias, cv * V + e);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int at = S::place(cv * V + e);
+                reinterpret_cast<float2*>(&sm.dx[tt][0])[at] = make_float2(d[e], d[e] * to_f(ru.v[e]));
+            }
+            if (back) {
+                const Pack<T, V> rz = sm.raw[slot][2][v][threadIdx.x], ro = sm.raw[slot][3][v][threadIdx.x];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float gg = to_f(ro.v[e]);
+                    if (p.z) gg *= to_f(rz.v[e]) * sigmoid_f<T>(to_f(rz.v[e]));
+                    reinterpret_cast<float*>(&sm.g[tt][0])[S::place(cv * V + e)] = gg;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k && !back) break;
+#pragma unroll
+            for (int i = 0; i < EB; ++i) {
+                const int e = i * kBwdThreads + threadIdx.x;
+                if (e < S::BC) {
+                    const Pack<T, BV> m = sm.rawbc[slot][k][i][threadIdx.x];
+                    float* to = &sm.bc[k][0][0] + e * BV;
+#pragma unroll
+                    for (int x = 0; x < BV; ++x) to[x] = to_f(m.v[x]);
+                }
+            }
+        }
+        __syncthreads();
+    };
+
+    // The tiles forwards, t0 .. last, and back from last to t0 are one sequence: the place that `ahead`
+    // would have if the way forwards went on.
+    const int last = t0 + (t1 - 1 - t0) / TL * TL;
+    auto fetch_ahead = [&](int ahead, int slot) {
+        const bool back = ahead > last;
+        fetch(back ? 2 * last + TL - ahead : ahead, slot, back);
+    };
+    fetch_ahead(t0, 0);
+    if constexpr (V > 1) fetch_ahead(t0 + TL, 1);
+    // states of a thread as packed pairs; a place without a channel stays zero throughout
+    uint64_t A2[CH][2], h[CH][2], mu[CH][2], dA[CH][2];
+    const uint64_t mean2 = pack2(kEx2Mean, kEx2Mean);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            A2[c][n] = live[c] ? pack2(p.A[cn0[c] + 2 * n] * kLog2e, p.A[cn0[c] + 2 * n + 1] * kLog2e) : 0ull;
+            h[c][n] = live[c] ? *reinterpret_cast<const uint64_t*>(ws.s.hs + wr * N + cn0[c] + 2 * n) : 0ull;
+            mu[c][n] = live[c] ? *reinterpret_cast<const uint64_t*>(ws.s.mu + wr * N + cn0[c] + 2 * n) : 0ull;
+            dA[c][n] = 0ull;
+        }
+
+    // forwards: the state before every 4th token
+    int slot = 0;
+    for (int t = t0; t < t1; t += TL, slot ^= 1) {
+        const int nt = min(TL, t1 - t);
+        arrive(slot, false);
+        if constexpr (V == 1) fetch_ahead(t + TL, 0);
+        for (int tt = 0; tt < nt; ++tt) {
+            if (tt % SUB == 0) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    *reinterpret_cast<ulonglong2*>(&sm.keep[(t - t0 + tt) / SUB][c][threadIdx.x]) = make_ulonglong2(h[c][0], h[c][1]);
+            }
+            if (t == last && tt >= (nt - 1) / SUB * SUB) break;   // the states behind are not asked for
+            const float4 d4 = sm.dx[tt][q];
+            const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w};
+            const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt][part * NS]);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]);
+                h[c][0] = fma2(ex2_2(fma2(A2[c][0], d2, mean2)), h[c][0], mul2(x2, bb.x));
+                h[c][1] = fma2(ex2_2(fma2(A2[c][1], d2, mean2)), h[c][1], mul2(x2, bb.y));
+            }
+        }
+        __syncthreads();
+        if constexpr (V > 1) fetch_ahead(t + 2 * TL, slot);
     }
-    Pack<T, V> ru[E::NV], rd[E::NV], ro[E::NV], rz[E::NV];
-    float acc_skip[E::NV][V], acc_bias[E::NV][V];
+    // backwards
+    float acc_skip[NV][V], acc_bias[NV][V];
 #pragma unroll
-    for (int v = 0; v < E::NV; ++v)
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < V; ++e) acc_skip[v][e] = acc_bias[v][e] = 0.f;
 
-    // stage tokens t .. t+15: dt, u (forward walk), and g, B, C
-    auto stage = [&](int t, int nt, bool back) {
+    for (int t = last; t >= t0; t -= TL, slot ^= 1) {
+        const int nt = min(TL, t1 - t);
+        arrive(slot, true);
+        if constexpr (V == 1) fetch(t - TL, 0, true);
+        auto sub = [&](int s0, int ns, auto full) {
+            constexpr bool FULL = decltype(full)::value;
+            uint64_t a[SUB][CH][2], hp[SUB][CH][2], hc[CH][2], accB[SUB][2], accC[SUB][2];
+            float v[SUB * 6];
 #pragma unroll
-        for (int v = 0; v < E::NV; ++v) {
-            const int i = v * kBwdThreads + threadIdx.x, tt = i / E::CV, c = i % E::CV * V;
-            if (tt >= kBwdTile) continue;
-            const bool ok = tt < nt && c < cn;
-            const size_t at = (row + t + tt) * D + c0 + c;
-            ru[v] = ok ? load_pack<T, V>((const T*)p.u + at) : zero_pack<T, V>();
-            rd[v] = ok ? load_pack<T, V>((const T*)p.dt + at) : zero_pack<T, V>();
-            if (back) {
-                ro[v] = ok ? load_pack<T, V>((const T*)p.dout + at) : zero_pack<T, V>();
-                rz[v] = ok && p.z ? load_pack<T, V>((const T*)p.z + at) : zero_pack<T, V>();
+            for (int c = 0; c < CH; ++c) {
+                const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sm.keep[(t - t0 + s0) / SUB][c][threadIdx.x]);
+                hc[c][0] = k2.x;
+                hc[c][1] = k2.y;
             }
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float bias = ok && p.dt_bias && c + e < cn ? p.dt_bias[c0 + c + e] : 0.f;
-                s_dt[tt][c + e] = softplus_f(to_f(rd[v].v[e]) + bias);
-                s_u[tt][c + e] = to_f(ru[v].v[e]);
-                if (back) {
-                    float gg = to_f(ro[v].v[e]);
-                    if (p.z) gg *= to_f(rz[v].v[e]) * sigmoid_f<T>(to_f(rz[v].v[e]));
-                    s_g[tt][c + e] = gg;
-                }
-            }
-        }
-        for (int i = threadIdx.x; i < kBwdTile * N; i += kBwdThreads) {
-            const int tt = i / N, n = i % N;
-            const size_t at = ((row + t + tt) * G + g) * N + n;
-            sB[tt][n] = tt < nt ? to_f(((const T*)p.Bm)[at]) : 0.f;
-            if (back) sC[tt][n] = tt < nt ? to_f(((const T*)p.Cm)[at]) : 0.f;
-        }
-    };
-
-    // forwards: the state at the start of every 8 tokens
-    for (int t = t0; t < t1; t += kBwdTile) {
-        const int nt = min(kBwdTile, t1 - t);
-        stage(t, nt, false);
-        __syncthreads();
-        for (int tt = 0; tt < nt; ++tt) {
-            if (tt % kBwdSub == 0)
-                keep[(size_t)((t - t0 + tt) / kBwdSub) * kBwdThreads + threadIdx.x] = make_float4(h[0], h[1], h[2], h[3]);
-            const float d = s_dt[tt][ch], x = d * s_u[tt][ch];
+            for (int k = 0; k < SUB; ++k) {
+                if (FULL || k < ns) {
+                    const float4 d4 = sm.dx[s0 + k][q];
+                    const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w};
+                    const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][s0 + k][part * NS]);
 #pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = fmaf(ex2_approx(A[n] * d), h[n], x * sB[tt][part * NS + n]);
-        }
-        __syncthreads();
-    }
-    // backwards
-    for (int t = t0 + (t1 - 1 - t0) / kBwdTile * kBwdTile; t >= t0; t -= kBwdTile) {
-        const int nt = min(kBwdTile, t1 - t);
-        stage(t, nt, true);
-        __syncthreads();
-        for (int s0 = (nt - 1) / kBwdSub * kBwdSub; s0 >= 0; s0 -= kBwdSub) {
-            const int ns = min(kBwdSub, nt - s0);
-            float a[kBwdSub][NS], hp[kBwdSub][NS], hc[NS];
-            const float4 k4 = keep[(size_t)((t - t0 + s0) / kBwdSub) * kBwdThreads + threadIdx.x];
-            hc[0] = k4.x; hc[1] = k4.y; hc[2] = k4.z; hc[3] = k4.w;
+                    for (int c = 0; c < CH; ++c) {
+                        const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]);
 #pragma unroll
-            for (int k = 0; k < kBwdSub; ++k) {
-                if (k < ns) {
-                    const float d = s_dt[s0 + k][ch], x = d * s_u[s0 + k][ch];
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        a[k][n] = ex2_approx(A[n] * d);
-                        hp[k][n] = hc[n];
-                        hc[n] = fmaf(a[k][n], hc[n], x * sB[s0 + k][part * NS + n]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = kBwdSub - 1; k >= 0; --k) {
-                if (k < ns) {
-                    const int tt = s0 + k;
-                    const float d = s_dt[tt][ch], uu = s_u[tt][ch], gg = s_g[tt][ch], x = d * uu;
-                    float y = 0.f, lb = 0.f, aq = 0.f, v[8];
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        const float Bn = sB[tt][part * NS + n], Cn = sC[tt][part * NS + n];
-                        const float lam = fmaf(Cn, gg, mu[n]);
-                        y = fmaf(hc[n], Cn, y);
-                        lb = fmaf(lam, Bn, lb);
-                        v[n] = live ? lam * x : 0.f;
-                        v[4 + n] = live ? gg * hc[n] : 0.f;
-                        mu[n] = a[k][n] * lam;
-                        const float q = mu[n] * hp[k][n];
-                        aq = fmaf(q, A[n], aq);
-                        dA[n] = fmaf(q, d, dA[n]);
-                        hc[n] = hp[k][n];
-                    }
-#pragma unroll
-                    for (int o = 1; o < LPC; o <<= 1) {
-                        y += __shfl_xor_sync(0xffffffffu, y, o);
-                        lb += __shfl_xor_sync(0xffffffffu, lb, o);
-                        aq += __shfl_xor_sync(0xffffffffu, aq, o);
-                    }
-                    if (part == 0) {
-                        s_dt[tt][ch] = lb;
-                        s_u[tt][ch] = aq * 0.6931471805599453f;   // A was scaled by log2 e
-                        s_g[tt][ch] = y;
-                    }
-                    LaneSum<8, LPC>::go(v);
-                    // the index of v[i]: dB or dC, state n, from the lane bits that chose the halves
-                    const int cb = (threadIdx.x % 32) / LPC;
-                    float* rr = red + ((size_t)warp * kBwdTile + tt) * 2 * N;
-                    const int first = (cb & 1 ? 4 : 0) + (CW > 2 && (cb & 2) ? 2 : 0) + (CW > 4 && (cb & 4) ? 1 : 0);
-                    if (CW <= 8 || cb < 8) {
-#pragma unroll
-                        for (int i = 0; i < LEFT; ++i) {
-                            const int j = first + i;
-                            rr[(j >= 4 ? N : 0) + part * NS + (j & 3)] = v[i];
+                        for (int n = 0; n < 2; ++n) {
+                            a[k][c][n] = ex2_2(fma2(A2[c][n], d2, mean2));
+                            hp[k][c][n] = hc[c][n];
+                            hc[c][n] = fma2(a[k][c][n], hc[c][n], mul2(x2, n ? bb.y : bb.x));
                         }
                     }
                 }
             }
+#pragma unroll
+            for (int k = SUB - 1; k >= 0; --k) {
+                if (FULL || k < ns) {
+                    const int tt = s0 + k;
+                    const float4 d4 = sm.dx[tt][q];
+                    const float2 g2f = sm.g[tt][q];
+                    const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w}, gg[CH] = {g2f.x, g2f.y};
+                    const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt][part * NS]);
+                    const ulonglong2 cc = *reinterpret_cast<const ulonglong2*>(&sm.bc[1][tt][part * NS]);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]), g2 = pack2(gg[c], gg[c]);
+                        uint64_t y2, lb2, aq2;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const uint64_t Bn = n ? bb.y : bb.x, Cn = n ? cc.y : cc.x;
+                            const uint64_t lam = fma2(Cn, g2, mu[c][n]);
+                            accB[k][n] = c ? fma2(lam, x2, accB[k][n]) : mul2(lam, x2);
+                            accC[k][n] = c ? fma2(hc[c][n], g2, accC[k][n]) : mul2(hc[c][n], g2);
+                            y2 = n ? fma2(hc[c][n], Cn, y2) : mul2(hc[c][n], Cn);
+                            lb2 = n ? fma2(lam, Bn, lb2) : mul2(lam, Bn);
+                            mu[c][n] = mul2(a[k][c][n], lam);
+                            const uint64_t qq = mul2(mu[c][n], hp[k][c][n]);
+                            aq2 = n ? fma2(qq, A2[c][n], aq2) : mul2(qq, A2[c][n]);
+                            dA[c][n] = fma2(qq, d2, dA[c][n]);
+                            hc[c][n] = hp[k][c][n];
+                        }
+                        float lo, hi;
+                        unpack2(y2, lo, hi);
+                        v[k * 6 + c] = lo + hi;
+                        unpack2(lb2, lo, hi);
+                        v[k * 6 + 2 + c] = lo + hi;
+                        unpack2(aq2, lo, hi);
+                        v[k * 6 + 4 + c] = lo + hi;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) v[k * 6 + i] = 0.f;
+                    accB[k][0] = accB[k][1] = accC[k][0] = accC[k][1] = 0ull;
+                }
+            }
+            // y, lambda B, A q of the 4 tokens' two channels, summed over a channel's lanes
+            constexpr int LEFT = lane_sum_left(SUB * 6, LPC);
+            int first = 0;
+            LaneSum<SUB * 6, 1, LPC>::go(v, first);
+            __syncwarp();   // every lane of the pair has read what is overwritten here
+#pragma unroll
+            for (int i = 0; i < LEFT; ++i) {
+                const int k = (first + i) / 6, j = (first + i) % 6;
+                if (!FULL && k >= ns) continue;
+                if (j < 4) reinterpret_cast<float*>(&sm.dx[s0 + k][q])[j] = v[i];
+                else reinterpret_cast<float*>(&sm.g[s0 + k][q])[j - 4] = v[i];
+            }
+            // dB, dC of the 4 tokens' 4 states, summed over the warp's channels
+            float w[SUB * 8];
+#pragma unroll
+            for (int k = 0; k < SUB; ++k)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    unpack2(accB[k][n], w[k * 8 + 2 * n], w[k * 8 + 2 * n + 1]);
+                    unpack2(accC[k][n], w[k * 8 + 4 + 2 * n], w[k * 8 + 4 + 2 * n + 1]);
+                }
+            constexpr int LEFTW = lane_sum_left(SUB * 8, 32 / LPC);
+            int fw = 0;
+            LaneSum<SUB * 8, LPC, 32>::go(w, fw);
+#pragma unroll
+            for (int i = 0; i < LEFTW; ++i) sm.red[warp][s0 + (fw + i) / 8][part][(fw + i) % 8] = w[i];
+        };
+        int s0 = (nt - 1) / SUB * SUB;
+        if (nt % SUB) {
+            sub(s0, nt - s0, std::false_type());
+            s0 -= SUB;
         }
+        for (; s0 >= 0; s0 -= SUB) sub(s0, SUB, std::true_type());
         __syncthreads();
         for (int i = threadIdx.x; i < nt * 2 * N; i += kBwdThreads) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) s += red[(size_t)w * kBwdTile * 2 * N + i];
+            for (int w = 0; w < S::W; ++w) s += (&sm.red[w][0][0][0])[i];
             const int tt = i / (2 * N), j = i % (2 * N);
             ws.bc[((((size_t)(tile % pl.tpg) * p.B + b) * p.L + t + tt) * G + g) * 2 * N + j] = s;
         }
 #pragma unroll
-        for (int v = 0; v < E::NV; ++v) {
-            const int i = v * kBwdThreads + threadIdx.x, tt = i / E::CV, c = i % E::CV * V;
-            if (tt >= nt || c >= cn) continue;
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * kBwdThreads + threadIdx.x, tt = i / CV, cv = i % CV;
+            if (i >= S::VECS || tt >= nt || cv * V >= cn) continue;
+            const Pack<T, V> ru = sm.raw[slot][0][v][threadIdx.x], rd = sm.raw[slot][1][v][threadIdx.x];
+            const Pack<T, V> rz = sm.raw[slot][2][v][threadIdx.x], ro = sm.raw[slot][3][v][threadIdx.x];
             Pack<T, V> ou, od, oz;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const int cc = c0 + c + e;
-                const float raw = to_f(rd[v].v[e]) + (p.dt_bias ? p.dt_bias[cc] : 0.f), sk = p.skip ? p.skip[cc] : 0.f;
-                const float d = softplus_f(raw), uu = to_f(ru[v].v[e]), oo = to_f(ro[v].v[e]);
-                const float lb = s_dt[tt][c + e], aq = s_u[tt][c + e];
+                const int at = S::place(cv * V + e), pr = at >> 1, hf = at & 1;
+                const float raw = to_f(rd.v[e]) + bias_at(p.dt_bias, cv * V + e), sk = bias_at(p.skip, cv * V + e);
+                const float d = softplus_f(raw), uu = to_f(ru.v[e]), oo = to_f(ro.v[e]);
+                const float y = reinterpret_cast<const float*>(&sm.dx[tt][pr])[hf];
+                const float lb = reinterpret_cast<const float*>(&sm.dx[tt][pr])[2 + hf];
+                const float aq = reinterpret_cast<const float*>(&sm.g[tt][pr])[hf] * 0.6931471805599453f;   // A was scaled by log2 e
                 float gg = oo;
                 if (p.z) {
-                    const float zz = to_f(rz[v].v[e]), sg = sigmoid_f<T>(zz);
+                    const float zz = to_f(rz.v[e]), sg = sigmoid_f<T>(zz);
                     gg *= zz * sg;
-                    from_f(oz.v[e], oo * fmaf(sk, uu, s_g[tt][c + e]) * (sg * (1.f + zz * (1.f - sg))));
+                    from_f(oz.v[e], oo * fmaf(sk, uu, y) * (sg * (1.f + zz * (1.f - sg))));
                 }
                 from_f(ou.v[e], fmaf(d, lb, sk * gg));
-                const float dr = fmaf(uu, lb, aq) / (1.f + expf(-raw));
+                const float dr = fmaf(uu, lb, aq) * sigmoid_f<float>(raw);
                 from_f(od.v[e], dr);
                 acc_skip[v][e] = fmaf(gg, uu, acc_skip[v][e]);
                 acc_bias[v][e] += dr;
             }
-            const size_t at = (row + t + tt) * D + c0 + c;
+            const size_t at = (row + t + tt) * D + c0 + cv * V;
             *reinterpret_cast<Pack<T, V>*>((T*)p.du + at) = ou;
             *reinterpret_cast<Pack<T, V>*>((T*)p.ddt + at) = od;
             if (p.z) *reinterpret_cast<Pack<T, V>*>((T*)p.dz + at) = oz;
         }
         __syncthreads();
+        if constexpr (V > 1) fetch(t - 2 * TL, slot, true);
     }
-    if (live) {
+    if constexpr (V > 1) copy_wait<0>();
 #pragma unroll
-        for (int n = 0; n < NS; ++n) ws.dA[wr * N + cn0 + n] = dA[n];
-    }
+    for (int c = 0; c < CH; ++c)
+        if (live[c])
+            *reinterpret_cast<ulonglong2*>(ws.dA + wr * N + cn0[c]) = make_ulonglong2(dA[c][0], dA[c][1]);
     // dskip, ddt_bias of the chunk: the element lanes' sums, added per channel in a fixed order
-    float* s_a = reinterpret_cast<float*>(keep);   // [tile rows][CPB], the kept states are done with
-    float* s_b = s_a + kBwdTile * CPB;
+    float* s_a = reinterpret_cast<float*>(&sm.keep[0][0][0]);   // [tile tokens][CPB]: the kept states are done with
+    float* s_b = s_a + TL * CPB;
 #pragma unroll
-    for (int v = 0; v < E::NV; ++v) {
-        const int i = v * kBwdThreads + threadIdx.x, tt = i / E::CV, c = i % E::CV * V;
-        if (tt >= kBwdTile) continue;
+    for (int v = 0; v < NV; ++v) {
+        const int i = v * kBwdThreads + threadIdx.x;
+        if (i >= S::VECS) break;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            s_a[tt * CPB + c + e] = acc_skip[v][e];
-            s_b[tt * CPB + c + e] = acc_bias[v][e];
+            s_a[i / CV * CPB + i % CV * V + e] = acc_skip[v][e];
+            s_b[i / CV * CPB + i % CV * V + e] = acc_bias[v][e];
         }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < cn; c += kBwdThreads) {
         float sa = 0.f, sb = 0.f;
 #pragma unroll
-        for (int tt = 0; tt < kBwdTile; ++tt) {
+        for (int tt = 0; tt < TL; ++tt) {
             sa += s_a[tt * CPB + c];
             sb += s_b[tt * CPB + c];
         }
@@ -450,8 +505,9 @@ __global__ void __launch_bounds__(256) k_bwd_bc(ScanArgs p, BwdPlan pl, BwdWs ws
     const int j = (int)(i % (2 * N)), t = (int)(tg / G % p.L), b = (int)(tg / G / p.L);
     if (t >= row_len(p.lens, b, p.L)) return;
     float s = 0.f;
+#pragma unroll 8
     for (int k = 0; k < pl.tpg; ++k) s += ws.bc[k * n + i];
-    T* o = j < N ? (T*)p.dB + tg * N + j : (T*)p.dC + tg * N + j - N;
+    T* o = (T*)(j & 4 ? p.dC : p.dB) + tg * N + j / 8 * 4 + (j & 3);
     from_f(*o, s);
 }
 
@@ -463,8 +519,10 @@ __global__ void __launch_bounds__(256) k_bwd_params(ScanArgs p, BwdWs ws, int ro
     const float* src = i < DN ? ws.dA + i : i < DN + D ? ws.dskip + (i - DN) : ws.dbias + (i - DN - D);
     const size_t step = i < DN ? DN : D;
     float acc = 0.f;
-    if (i < all)
+    if (i < all) {
+#pragma unroll 4
         for (int r = y; r < rows; r += 8) acc += src[r * step];
+    }
     s[y][lane] = acc;
     __syncthreads();
     if (y || i >= all) return;
@@ -476,46 +534,41 @@ __global__ void __launch_bounds__(256) k_bwd_params(ScanArgs p, BwdWs ws, int ro
 }
 
 template <typename T, int N, int V>
-static favor_status bwd_launch(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
-    const BwdPlan pl = bwd_plan(h, a.L);
-    size_t total = 0;
-    const BwdWs ws = bwd_layout(h.ws, pl, a.B, a.L, h.D, N, h.G, &total);
-    const unsigned grid = (unsigned)pl.tiles * a.B * pl.nC;
-    constexpr int CPB = Elems<T, N, V, kBwdTile>::CPB;
-    const size_t smem = (size_t)(kBwdChunk / kBwdSub) * kBwdThreads * 16 + 3 * kBwdTile * CPB * 4 +
-                        2 * kBwdTile * N * 4 + (size_t)(kBwdThreads / 32) * kBwdTile * 2 * N * 4;
-    if (cudaFuncSetAttribute(k_bwd_main<T, N, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return check_launch("favor_ssm_scan_backward");
-    k_bwd_summary<T, N, V><<<grid, kBwdThreads, 0, st>>>(a, pl, ws, h.D, h.G);
-    const size_t chain = (size_t)a.B * h.D * N;
-    k_bwd_chain<<<(unsigned)((chain + 255) / 256), 256, 0, st>>>(a, pl, ws, h.D, N);
-    k_bwd_main<T, N, V><<<grid, kBwdThreads, smem, st>>>(a, pl, ws, h.D, h.G);
-    const size_t bc = (size_t)a.B * a.L * h.G * 2 * N;
-    k_bwd_bc<T><<<(unsigned)((bc + 255) / 256), 256, 0, st>>>(a, pl, ws, N, h.G);
-    const size_t par = (size_t)h.D * (N + 2);
-    k_bwd_params<<<(unsigned)((par + 31) / 32), 256, 0, st>>>(a, ws, a.B * pl.nC, h.D, N);
-    count_launch(5);
-    return check_launch("favor_ssm_scan_backward");
+static void bwd_launch(const SsmHandle& h, const ScanArgs& a, const BwdPlan& pl, const BwdWs& ws, cudaStream_t st) {
+    using S = BwdShared<T, N, V>;
+    static_assert(sizeof(float4) * (S::CHUNK / kBwdSub) * kBwdCH * kBwdThreads >= 2 * kBwdTile * S::CPB * sizeof(float),
+                  "the last sums are made where the kept states were");
+    // the attribute's failure shows as the launch's
+    cudaFuncSetAttribute(k_bwd_main<T, N, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S));
+    k_bwd_main<T, N, V><<<(unsigned)pl.tiles * a.B * pl.nC, kBwdThreads, sizeof(S), st>>>(a, pl, ws, h.D, h.G);
 }
 
 template <typename T, int V>
-static favor_status bwd_by_n(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
-    if (h.N == 8) return bwd_launch<T, 8, V>(h, a, st);
-    if (h.N == 16) return bwd_launch<T, 16, V>(h, a, st);
-    if (h.N == 32) return bwd_launch<T, 32, V>(h, a, st);
-    return bwd_launch<T, 64, V>(h, a, st);
+static void bwd_by_n(const SsmHandle& h, const ScanArgs& a, const BwdPlan& pl, const BwdWs& ws, cudaStream_t st) {
+    if (h.N == 8) bwd_launch<T, 8, V>(h, a, pl, ws, st);
+    else if (h.N == 16) bwd_launch<T, 16, V>(h, a, pl, ws, st);
+    else if (h.N == 32) bwd_launch<T, 32, V>(h, a, pl, ws, st);
+    else bwd_launch<T, 64, V>(h, a, pl, ws, st);
 }
 
 favor_status scan_backward(const SsmHandle& h, const ScanArgs& a, cudaStream_t st) {
     const bool f32 = h.dtype == FAVOR_DTYPE_F32;
-    const int v = 4;
-    const bool vec = h.D % v == 0 && (h.D / h.G) % v == 0 && is_aligned16(a.u) && is_aligned16(a.dt) &&
-                     is_aligned16(a.z) && is_aligned16(a.dout) && is_aligned16(a.du) && is_aligned16(a.ddt) &&
-                     is_aligned16(a.dz);
-    if (f32 && vec) return bwd_by_n<float, 4>(h, a, st);
-    if (f32) return bwd_by_n<float, 1>(h, a, st);
-    if (vec) return bwd_by_n<__nv_bfloat16, 4>(h, a, st);
-    return bwd_by_n<__nv_bfloat16, 1>(h, a, st);
+    const BwdPlan pl = bwd_plan(h, a.L);
+    size_t total = 0;
+    const BwdWs ws = bwd_layout(h.ws, pl, a.B, a.L, h.D, h.N, h.G, &total);
+    const bool vec = scan_grad_chunks(h, a, ws.s, bwd_chunk(h), st);
+    if (f32 && vec) bwd_by_n<float, 4>(h, a, pl, ws, st);
+    else if (f32) bwd_by_n<float, 1>(h, a, pl, ws, st);
+    else if (vec) bwd_by_n<__nv_bfloat16, 8>(h, a, pl, ws, st);
+    else bwd_by_n<__nv_bfloat16, 1>(h, a, pl, ws, st);
+    const size_t bc = (size_t)a.B * a.L * h.G * 2 * h.N;
+    const unsigned grid = (unsigned)((bc + 255) / 256);
+    if (f32) k_bwd_bc<float><<<grid, 256, 0, st>>>(a, pl, ws, h.N, h.G);
+    else k_bwd_bc<__nv_bfloat16><<<grid, 256, 0, st>>>(a, pl, ws, h.N, h.G);
+    const size_t par = (size_t)h.D * (h.N + 2);
+    k_bwd_params<<<(unsigned)((par + 31) / 32), 256, 0, st>>>(a, ws, a.B * pl.nC, h.D, h.N);
+    count_launch(3);
+    return check_launch("favor_ssm_scan_backward");
 }
 
 }  // namespace favor

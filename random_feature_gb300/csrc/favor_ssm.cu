@@ -89,6 +89,8 @@ favor_status favor_ssm_create(favor_ssm* out, int D, int N, int G, int K, favor_
     if (K < 2 || K > 4) return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: K=%d (supported: 2, 3, 4)", K);
     if (D > (1 << 20) || (long long)max_B * max_L > (1LL << 30) || (long long)max_B * max_L > (1LL << 36) / D)
         return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: D or max_B*max_L*D too large");
+    if ((long long)max_B * N > (1LL << 36) / D || (long long)max_B * max_L * N > (1LL << 36) / G)
+        return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: max_B*D*N or max_B*max_L*G*N too large");
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();

@@ -63,6 +63,16 @@ favor_status scan_prompt(const SsmHandle& h, const ScanArgs& a, cudaStream_t st)
 favor_status scan_step(const SsmHandle& h, const ScanArgs& a, cudaStream_t st);
 favor_status scan_backward(const SsmHandle& h, const ScanArgs& a, cudaStream_t st);
 
+// Per chunk of tokens, in the workspace (see favor_scan.cu).
+struct ScanWs {
+    float* hs;      // [B][nC][D][N] the chunk's own end, then its start
+    float* sdt;     // [B][nC][D] sum of dt
+    float* mu;      // [B][nC][D][N] backward: what it hands back, then what it is handed
+};
+// Chunk starts and incoming gradients of a backward call with chunks of Lc tokens; whether its rows
+// take 16-byte accesses.
+bool scan_grad_chunks(const SsmHandle& h, const ScanArgs& a, const ScanWs& ws, int Lc, cudaStream_t st);
+
 // Workspace (floats) the calls of a handle with these sizes can need.
 size_t scan_prompt_ws(const SsmHandle& h);
 size_t scan_backward_ws(const SsmHandle& h);
