@@ -36,6 +36,7 @@ struct ScanPlan {
     int tpg;       // channel tiles a group
     int Dg;        // channels a group
     int nC, Lc;    // chunks, tokens a chunk
+    int per;       // chunks a block (SCAN_GRAD; else 1)
 };
 
 // MODE: SCAN_OUT writes the outputs.  Where a row has several chunks they start
@@ -87,9 +88,10 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     S& sm = *reinterpret_cast<S*>(smem);
 
     const int tile = blockIdx.x % pl.tiles, rest = blockIdx.x / pl.tiles;
-    const int b = rest % p.B, chunk = rest / p.B;
+    const int b = rest % p.B;
+    int chunk = rest / p.B * pl.per;
     const int len = row_len(p.lens, b, p.L);
-    const int t0 = chunk * pl.Lc, t1 = min(t0 + pl.Lc, len);
+    const int t0 = chunk * pl.Lc, t1 = min(t0 + pl.Lc * pl.per, len);
     if (t0 >= t1 || (MODE == SCAN_SUM && t1 == len)) return;
     const int page = OUT && p.state ? block_page(p.pg, b) : 0;
     const int g = tile / pl.tpg, cl = (tile % pl.tpg) * CPB, c0 = g * pl.Dg + cl, cn = min(CPB, pl.Dg - cl);
@@ -293,6 +295,34 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         }
         return r;
     };
+    // the state (OUT: into the page by the row's last chunk; else, with the sum of dt, into the workspace)
+    auto leave = [&]() {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (!live[c]) continue;
+            const size_t r = ((size_t)b * pl.nC + chunk) * D;
+            float* to = !OUT ? ws.hs + r * N : stp && t1 == len ? stp : nullptr;
+#pragma unroll
+            for (int n = 0; n < NS / 2; ++n) {
+                if (to) *reinterpret_cast<uint64_t*>(to + cn0[c] + 2 * n) = h[c][n];
+                if (GRAD) *reinterpret_cast<uint64_t*>(ws.mu + r * N + cn0[c] + 2 * n) = mu[c][n];
+            }
+            if (!OUT && part == 0) ws.sdt[r + c0 + ch[c]] = total_dt[c];
+        }
+    };
+    auto next_chunk = [&]() {
+        leave();
+        ++chunk;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            total_dt[c] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NS / 2; ++n) {
+                h[c][n] = mu[GRAD ? c : 0][n] = 0ull;
+                P[GRAD ? c : 0][n] = pack2(1.f, 1.f);
+            }
+        }
+    };
     int slot = 0;
     for (int t = t0; t < t1; t += TT, slot ^= 1) {
         const int nt = min(TT, t1 - t);
@@ -337,6 +367,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         if constexpr (V == 1) fetch(t + TT, 0);
         int tt = 0;
         for (; tt + UN <= nt; tt += UN) {
+            if (GRAD && t + tt == t0 + (chunk - rest / p.B * pl.per + 1) * pl.Lc) next_chunk();
             float y[UN * CH];
             tokens(tt, std::integral_constant<int, UN>(), y);
             if (OUT) {
@@ -345,6 +376,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
             }
         }
         for (; tt < nt; tt += GK) {
+            if (GRAD && t + tt == t0 + (chunk - rest / p.B * pl.per + 1) * pl.Lc) next_chunk();
             float y[GK * CH] = {};
 #pragma unroll
             for (int k = 0; k < GK; ++k)
@@ -374,18 +406,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         if constexpr (V > 1) fetch(t + 2 * TT, slot);
     }
     if constexpr (V > 1) copy_wait<0>();
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        if (!live[c]) continue;
-        const size_t r = ((size_t)b * pl.nC + chunk) * D;
-        float* to = !OUT ? ws.hs + r * N : stp && t1 == len ? stp : nullptr;
-#pragma unroll
-        for (int n = 0; n < NS / 2; ++n) {
-            if (to) *reinterpret_cast<uint64_t*>(to + cn0[c] + 2 * n) = h[c][n];
-            if (GRAD) *reinterpret_cast<uint64_t*>(ws.mu + r * N + cn0[c] + 2 * n) = mu[c][n];
-        }
-        if (!OUT && part == 0) ws.sdt[r + c0 + ch[c]] = total_dt[c];
-    }
+    leave();
 }
 
 // Per (row, channel, state), in the chunks' order: ws.hs from each chunk's own end to
@@ -402,37 +423,44 @@ __global__ void __launch_bounds__(128) k_scan_chain(ScanArgs p, ScanPlan pl, Sca
     const size_t r = (size_t)b * pl.nC;
     const float* sdt = ws.sdt + r * D + c;
     float h = !GRAD && p.state ? p.state[(size_t)page * DN + i] : 0.f, mu = 0.f;
-    float* hs = ws.hs + r * DN + i;
-    for (int j0 = 0; j0 < used; j0 += 8) {
-        float e[8], s[8];
+    float *hs = ws.hs + r * DN + i, *ms = GRAD ? ws.mu + r * DN + i : nullptr;
+    constexpr int K = 8;
+    float e[K], s[K], f[K], w[K];   // chunks j0 .., and (backward call) used-1-j0, downwards
+    auto fetch = [&](int j0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const bool in = j0 + k < used - 1;   // the last one's own end is not asked for
-            e[k] = in ? hs[(size_t)(j0 + k) * DN] : 0.f;
-            s[k] = in ? sdt[(size_t)(j0 + k) * D] : 0.f;
+        for (int k = 0; k < K; ++k) {
+            const bool in = j0 + k < used - 1;   // the last one's own end is not asked for, nor what the first hands back
+            const int j = in ? j0 + k : 0, m = in ? used - 1 - j0 - k : 0;
+            e[k] = in ? hs[(size_t)j * DN] : 0.f;
+            s[k] = in ? sdt[(size_t)j * D] : 0.f;
+            if (GRAD) {
+                f[k] = in ? ms[(size_t)m * DN] : 0.f;
+                w[k] = in ? sdt[(size_t)m * D] : 0.f;
+            }
         }
+    };
+    fetch(0);
+    for (int j0 = 0; j0 < used; j0 += K) {
+        float e0[K], s0[K], f0[K], w0[K];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < K; ++k) {
+            e0[k] = e[k];
+            s0[k] = ex2_approx(A * s[k]);
+            if (GRAD) {
+                f0[k] = f[k];
+                w0[k] = ex2_approx(A * w[k]);
+            }
+        }
+        fetch(j0 + K);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
             if (j0 + k >= used) break;
             hs[(size_t)(j0 + k) * DN] = h;
-            h = fmaf(ex2_approx(A * s[k]), h, e[k]);
-        }
-    }
-    if (!GRAD) return;
-    float* ms = ws.mu + r * DN + i;
-    for (int j0 = used - 1; j0 >= 0; j0 -= 8) {
-        float e[8], s[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const bool in = j0 - k > 0;   // the first one hands to nobody
-            e[k] = in ? ms[(size_t)(j0 - k) * DN] : 0.f;
-            s[k] = in ? sdt[(size_t)(j0 - k) * D] : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (j0 - k < 0) break;
-            ms[(size_t)(j0 - k) * DN] = mu;
-            mu = fmaf(ex2_approx(A * s[k]), mu, e[k]);
+            h = fmaf(s0[k], h, e0[k]);
+            if (GRAD) {
+                ms[(size_t)(used - 1 - j0 - k) * DN] = mu;
+                mu = fmaf(w0[k], mu, f0[k]);
+            }
         }
     }
 }
@@ -544,6 +572,7 @@ static ScanPlan scan_plan(const SsmHandle& h, int B, int L, int CPB, int TT) {
     pl.Lc = (int)((L + want - 1) / want);
     pl.Lc = (pl.Lc + TT - 1) / TT * TT;
     pl.nC = (L + pl.Lc - 1) / pl.Lc;
+    pl.per = 1;
     return pl;
 }
 
@@ -582,8 +611,12 @@ static void grad_launch(const SsmHandle& h, const ScanArgs& a, const ScanWs& ws,
     pl.tiles = pl.tpg * h.G;
     pl.Lc = Lc;
     pl.nC = (a.L + Lc - 1) / Lc;
+    // chunks a block: up to 256 tokens while there are blocks for two waves
+    pl.per = 1;
+    while (pl.per * Lc < 256 && (long long)pl.tiles * a.B * (pl.nC / pl.per) >= 4LL * h.num_sms * kScanPerSm) pl.per *= 2;
     cudaFuncSetAttribute(k_scan<T, N, V, SCAN_GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S));
-    k_scan<T, N, V, SCAN_GRAD><<<(unsigned)pl.tiles * a.B * pl.nC, kScanThreads, sizeof(S), st>>>(a, pl, ws, h.D, h.G);
+    k_scan<T, N, V, SCAN_GRAD><<<(unsigned)pl.tiles * a.B * ((pl.nC + pl.per - 1) / pl.per), kScanThreads, sizeof(S), st>>>(a, pl, ws, h.D,
+                                                                                                      h.G);
     k_scan_chain<true><<<(unsigned)((h.D * N + 127) / 128) * a.B, 128, 0, st>>>(a, pl, ws, h.D, N);
     count_launch(2);
 }

@@ -17,8 +17,8 @@
 #include "ssm_internal.h"
 
 #ifndef BCH
-#define BCH 64
-#define BMB 2
+#define BCH 32
+#define BMB 3
 #endif
 namespace favor {
 
@@ -28,7 +28,7 @@ constexpr int kBwdTile = 16;        // tokens staged in shared memory at a time
 constexpr int kBwdNS = 4;           // states a thread, of
 constexpr int kBwdCH = 2;           // channels
 // Tokens of a chunk: the kept states take 8 KB for every 4 of them.
-template <typename T> struct BwdChunk { static constexpr int value = sizeof(T) == 2 ? BCH : 32; };
+constexpr int kBwdChunk = BCH;
 
 struct BwdPlan {
     int tiles, tpg, Dg, nC;
@@ -57,17 +57,13 @@ static BwdWs bwd_layout(float* ws, const BwdPlan& pl, int B, int L, int D, int N
     return w;
 }
 
-static int bwd_chunk(const SsmHandle& h) {
-    return h.dtype == FAVOR_DTYPE_F32 ? BwdChunk<float>::value : BwdChunk<__nv_bfloat16>::value;
-}
-
 static BwdPlan bwd_plan(const SsmHandle& h, int L) {
     BwdPlan pl;
     const int CPB = kBwdThreads * kBwdNS * kBwdCH / h.N;
     pl.Dg = h.D / h.G;
     pl.tpg = (pl.Dg + CPB - 1) / CPB;
     pl.tiles = pl.tpg * h.G;
-    pl.nC = (L + bwd_chunk(h) - 1) / bwd_chunk(h);
+    pl.nC = (L + kBwdChunk - 1) / kBwdChunk;
     return pl;
 }
 
@@ -83,7 +79,7 @@ size_t scan_backward_ws(const SsmHandle& h) {
 // becomes the index of the lane's v[0].
 template <int W, int BIT, int END>
 struct LaneSum {
-    static __device__ __forceinline__ void go(float* v, int& first) {
+    static __device__ __forceinline__ void go(float* v, unsigned& first) {
         if constexpr (BIT < END) {
             if constexpr (W % 2 == 0) {
                 const bool up = threadIdx.x & BIT;
@@ -107,7 +103,7 @@ constexpr int lane_sum_left(int W, int lanes) { return lanes > 1 && W % 2 == 0 ?
 template <typename T, int N, int V>
 struct BwdShared {
     static constexpr int LPC = N / kBwdNS, CPB = kBwdThreads * kBwdCH / LPC, PAIRS = CPB / 2, CV = CPB / V;
-    static constexpr int CHUNK = BwdChunk<T>::value, W = kBwdThreads / 32;
+    static constexpr int CHUNK = kBwdChunk, W = kBwdThreads / 32;
     // Channel cl of a tile sits at place (cl % VP) (CPB / VP) + cl / VP of a shared row, as in the
     // forward kernel; the narrow path keeps the places, and with them the order of the sums.
     static constexpr int VP = 16 / (int)sizeof(T), PV = CPB / VP;
@@ -115,15 +111,16 @@ struct BwdShared {
     static constexpr int VECS = kBwdTile * CV, NV = (VECS + kBwdThreads - 1) / kBwdThreads;
     static constexpr int BV = V > 1 ? 16 / (int)sizeof(T) : 1;
     static constexpr int BC = kBwdTile * N / BV, EB = (BC + kBwdThreads - 1) / kBwdThreads;
-    static constexpr int PAD = 1;
+    static constexpr int PAD = PV < 16 ? PV / 2 : 4;   // the rows that one warp's element lanes touch start on other banks
     float4 keep[CHUNK / kBwdSub][kBwdCH][kBwdThreads];
-    // a channel pair's (dt, dt u) twice and its g; then y twice, lambda B twice and A q
+    // of a channel pair, each: (dt, dt u) and g, then (y, lambda B) and A q
     float4 dx[kBwdTile][PAIRS + PAD];
     float2 g[kBwdTile][PAIRS + PAD];
     alignas(16) float bc[2][kBwdTile][N];
     alignas(16) float red[W][kBwdTile][LPC][8];
     Pack<T, V> raw[2][4][NV][kBwdThreads];
-    Pack<T, BV> rawbc[2][2][EB][kBwdThreads];
+    Pack<T, BV> rawbc[2][2][EB > 1 ? EB * kBwdThreads : BC];
+    alignas(16) float sbias[CPB], sskip[CPB];   // by place
 };
 
 template <typename T, int N, int V>
@@ -189,7 +186,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
                 const bool ok = e < S::BC && t >= t0 && t + tt < t1;
                 const T* at = ok ? mat[k] + (size_t)(t + tt) * G * N + n : mat[k];
                 if constexpr (V > 1) {
-                    copy_async(&sm.rawbc[slot][k][i][threadIdx.x], at, ok);
+                    if (e < S::BC) copy_async(&sm.rawbc[slot][k][e], at, ok);
                 } else {
                     from_f(rbc[k][i], 0.f);
                     if (ok) rbc[k][i] = *at;
@@ -198,7 +195,6 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
         }
         if constexpr (V > 1) copy_commit();
     };
-    auto bias_at = [&](const float* f, int c) { return f && c < cn ? f[c0 + c] : 0.f; };
     // the tile's elements arrive: dt, dt u (and g) for the state lanes, B (and C)
     auto arrive = [&](int slot, bool back) {
         if constexpr (V > 1) {
@@ -214,7 +210,10 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             for (int k = 0; k < 2; ++k) {
                 if (k && !back) break;
 #pragma unroll
-                for (int i = 0; i < EB; ++i) sm.rawbc[slot][k][i][threadIdx.x].v[0] = rbc[k][i];
+                for (int i = 0; i < EB; ++i) {
+                    const int e = i * kBwdThreads + threadIdx.x;
+                    if (e < S::BC) sm.rawbc[slot][k][e].v[0] = rbc[k][i];
+                }
             }
         }
 #pragma unroll
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             float d[V + V % 2];
             if constexpr (V == 1) d[1] = 0.f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) d[e] = to_f(rd.v[e]) + bias_at(p.dt_bias, cv * V + e);
+            for (int e = 0; e < V; ++e) d[e] = to_f(rd.v[e]) + sm.sbias[S::place(cv * V + e)];
 #pragma unroll
             for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
 #pragma unroll
@@ -250,7 +249,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             for (int i = 0; i < EB; ++i) {
                 const int e = i * kBwdThreads + threadIdx.x;
                 if (e < S::BC) {
-                    const Pack<T, BV> m = sm.rawbc[slot][k][i][threadIdx.x];
+                    const Pack<T, BV> m = sm.rawbc[slot][k][e];
                     float* to = &sm.bc[k][0][0] + e * BV;
 #pragma unroll
                     for (int x = 0; x < BV; ++x) to[x] = to_f(m.v[x]);
@@ -267,6 +266,10 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
         const bool back = ahead > last;
         fetch(back ? 2 * last + TL - ahead : ahead, slot, back);
     };
+    for (int c = threadIdx.x; c < CPB; c += kBwdThreads) {
+        sm.sbias[S::place(c)] = c < cn && p.dt_bias ? p.dt_bias[c0 + c] : 0.f;
+        sm.sskip[S::place(c)] = c < cn && p.skip ? p.skip[c0 + c] : 0.f;
+    }
     fetch_ahead(t0, 0);
     if constexpr (V > 1) fetch_ahead(t0 + TL, 1);
     // states of a thread as packed pairs; a place without a channel stays zero throughout
@@ -281,6 +284,8 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             mu[c][n] = live[c] ? *reinterpret_cast<const uint64_t*>(ws.s.mu + wr * N + cn0[c] + 2 * n) : 0ull;
             dA[c][n] = 0ull;
         }
+
+    __syncthreads();   // sbias
 
     // forwards: the state before every 4th token
     int slot = 0;
@@ -309,11 +314,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
         if constexpr (V > 1) fetch_ahead(t + 2 * TL, slot);
     }
     // backwards
-    float acc_skip[NV][V], acc_bias[NV][V];
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc_skip[v][e] = acc_bias[v][e] = 0.f;
+    float dskip = 0.f, dbias = 0.f;   // of the channel at place threadIdx.x
 
     for (int t = last; t >= t0; t -= TL, slot ^= 1) {
         const int nt = min(TL, t1 - t);
@@ -321,84 +322,78 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
         if constexpr (V == 1) fetch(t - TL, 0, true);
         auto sub = [&](int s0, int ns, auto full) {
             constexpr bool FULL = decltype(full)::value;
-            uint64_t a[SUB][CH][2], hp[SUB][CH][2], hc[CH][2], accB[SUB][2], accC[SUB][2];
-            float v[SUB * 6];
+            uint64_t accB[SUB][2], accC[SUB][2];
+            // one channel after the other: decays and states of both at once would take 64 registers more
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
+                uint64_t a[SUB][2], hp[SUB][2], hc[2];
+                float v[SUB * 3];
                 const ulonglong2 k2 = *reinterpret_cast<const ulonglong2*>(&sm.keep[(t - t0 + s0) / SUB][c][threadIdx.x]);
-                hc[c][0] = k2.x;
-                hc[c][1] = k2.y;
-            }
+                hc[0] = k2.x;
+                hc[1] = k2.y;
 #pragma unroll
-            for (int k = 0; k < SUB; ++k) {
-                if (FULL || k < ns) {
-                    const float4 d4 = sm.dx[s0 + k][q];
-                    const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w};
-                    const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][s0 + k][part * NS]);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]);
+                for (int k = 0; k < SUB; ++k) {
+                    if (FULL || k < ns) {
+                        const float2 dx = reinterpret_cast<const float2*>(&sm.dx[s0 + k][q])[c];
+                        const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][s0 + k][part * NS]);
+                        const uint64_t d2 = pack2(dx.x, dx.x), x2 = pack2(dx.y, dx.y);
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            a[k][c][n] = ex2_2(fma2(A2[c][n], d2, mean2));
-                            hp[k][c][n] = hc[c][n];
-                            hc[c][n] = fma2(a[k][c][n], hc[c][n], mul2(x2, n ? bb.y : bb.x));
+                            a[k][n] = ex2_2(fma2(A2[c][n], d2, mean2));
+                            hp[k][n] = hc[n];
+                            hc[n] = fma2(a[k][n], hc[n], mul2(x2, n ? bb.y : bb.x));
                         }
                     }
                 }
-            }
 #pragma unroll
-            for (int k = SUB - 1; k >= 0; --k) {
-                if (FULL || k < ns) {
-                    const int tt = s0 + k;
-                    const float4 d4 = sm.dx[tt][q];
-                    const float2 g2f = sm.g[tt][q];
-                    const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w}, gg[CH] = {g2f.x, g2f.y};
-                    const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt][part * NS]);
-                    const ulonglong2 cc = *reinterpret_cast<const ulonglong2*>(&sm.bc[1][tt][part * NS]);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]), g2 = pack2(gg[c], gg[c]);
+                for (int k = SUB - 1; k >= 0; --k) {
+                    if (FULL || k < ns) {
+                        const int tt = s0 + k;
+                        const float2 dx = reinterpret_cast<const float2*>(&sm.dx[tt][q])[c];
+                        const float gg = reinterpret_cast<const float*>(&sm.g[tt][q])[c];
+                        const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt][part * NS]);
+                        const ulonglong2 cc = *reinterpret_cast<const ulonglong2*>(&sm.bc[1][tt][part * NS]);
+                        const uint64_t d2 = pack2(dx.x, dx.x), x2 = pack2(dx.y, dx.y), g2 = pack2(gg, gg);
                         uint64_t y2, lb2, aq2;
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             const uint64_t Bn = n ? bb.y : bb.x, Cn = n ? cc.y : cc.x;
                             const uint64_t lam = fma2(Cn, g2, mu[c][n]);
                             accB[k][n] = c ? fma2(lam, x2, accB[k][n]) : mul2(lam, x2);
-                            accC[k][n] = c ? fma2(hc[c][n], g2, accC[k][n]) : mul2(hc[c][n], g2);
-                            y2 = n ? fma2(hc[c][n], Cn, y2) : mul2(hc[c][n], Cn);
+                            accC[k][n] = c ? fma2(hc[n], g2, accC[k][n]) : mul2(hc[n], g2);
+                            y2 = n ? fma2(hc[n], Cn, y2) : mul2(hc[n], Cn);
                             lb2 = n ? fma2(lam, Bn, lb2) : mul2(lam, Bn);
-                            mu[c][n] = mul2(a[k][c][n], lam);
-                            const uint64_t qq = mul2(mu[c][n], hp[k][c][n]);
+                            mu[c][n] = mul2(a[k][n], lam);
+                            const uint64_t qq = mul2(mu[c][n], hp[k][n]);
                             aq2 = n ? fma2(qq, A2[c][n], aq2) : mul2(qq, A2[c][n]);
                             dA[c][n] = fma2(qq, d2, dA[c][n]);
-                            hc[c][n] = hp[k][c][n];
+                            hc[n] = hp[k][n];
                         }
                         float lo, hi;
                         unpack2(y2, lo, hi);
-                        v[k * 6 + c] = lo + hi;
+                        v[k * 3] = lo + hi;
                         unpack2(lb2, lo, hi);
-                        v[k * 6 + 2 + c] = lo + hi;
+                        v[k * 3 + 1] = lo + hi;
                         unpack2(aq2, lo, hi);
-                        v[k * 6 + 4 + c] = lo + hi;
+                        v[k * 3 + 2] = lo + hi;
+                    } else {
+                        v[k * 3] = v[k * 3 + 1] = v[k * 3 + 2] = 0.f;
+                        accB[k][0] = accB[k][1] = accC[k][0] = accC[k][1] = 0ull;
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) v[k * 6 + i] = 0.f;
-                    accB[k][0] = accB[k][1] = accC[k][0] = accC[k][1] = 0ull;
                 }
-            }
-            // y, lambda B, A q of the 4 tokens' two channels, summed over a channel's lanes
-            constexpr int LEFT = lane_sum_left(SUB * 6, LPC);
-            int first = 0;
-            LaneSum<SUB * 6, 1, LPC>::go(v, first);
-            __syncwarp();   // every lane of the pair has read what is overwritten here
+                // y, lambda B, A q of the 4 tokens, summed over the channel's lanes
+                constexpr int LEFT = lane_sum_left(SUB * 3, LPC);
+                static_assert(LEFT % 3 == 0, "whole tokens are left with a lane");
+                unsigned first = 0;
+                LaneSum<SUB * 3, 1, LPC>::go(v, first);
+                __syncwarp();   // every lane of the channel has read what is overwritten here
 #pragma unroll
-            for (int i = 0; i < LEFT; ++i) {
-                const int k = (first + i) / 6, j = (first + i) % 6;
-                if (!FULL && k >= ns) continue;
-                if (j < 4) reinterpret_cast<float*>(&sm.dx[s0 + k][q])[j] = v[i];
-                else reinterpret_cast<float*>(&sm.g[s0 + k][q])[j - 4] = v[i];
+                for (int i = 0; i < LEFT; ++i) {
+                    const int k = first / 3 + i / 3, j = i % 3;
+                    if (!FULL && k >= ns) continue;
+                    if (j < 2) reinterpret_cast<float*>(&sm.dx[s0 + k][q])[c * 2 + j] = v[i];
+                    else reinterpret_cast<float*>(&sm.g[s0 + k][q])[c] = v[i];
+                }
             }
             // dB, dC of the 4 tokens' 4 states, summed over the warp's channels
             float w[SUB * 8];
@@ -410,10 +405,17 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
                     unpack2(accC[k][n], w[k * 8 + 4 + 2 * n], w[k * 8 + 4 + 2 * n + 1]);
                 }
             constexpr int LEFTW = lane_sum_left(SUB * 8, 32 / LPC);
-            int fw = 0;
+            unsigned fw = 0;   // a multiple of LEFTW
             LaneSum<SUB * 8, LPC, 32>::go(w, fw);
+            if constexpr (LEFTW % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < LEFTW; ++i) sm.red[warp][s0 + (fw + i) / 8][part][(fw + i) % 8] = w[i];
+                for (int i = 0; i < LEFTW; i += 4)
+                    *reinterpret_cast<float4*>(&sm.red[warp][s0 + fw / 8 + i / 8][part][fw % 8 + i % 8]) =
+                        make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < LEFTW; ++i) sm.red[warp][s0 + fw / 8][part][fw % 8 + i] = w[i];
+            }
         };
         int s0 = (nt - 1) / SUB * SUB;
         if (nt % SUB) {
@@ -439,10 +441,10 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const int at = S::place(cv * V + e), pr = at >> 1, hf = at & 1;
-                const float raw = to_f(rd.v[e]) + bias_at(p.dt_bias, cv * V + e), sk = bias_at(p.skip, cv * V + e);
+                const float raw = to_f(rd.v[e]) + sm.sbias[at], sk = sm.sskip[at];
                 const float d = softplus_f(raw), uu = to_f(ru.v[e]), oo = to_f(ro.v[e]);
-                const float y = reinterpret_cast<const float*>(&sm.dx[tt][pr])[hf];
-                const float lb = reinterpret_cast<const float*>(&sm.dx[tt][pr])[2 + hf];
+                const float2 yl = reinterpret_cast<const float2*>(&sm.dx[tt][pr])[hf];
+                const float y = yl.x, lb = yl.y;
                 const float aq = reinterpret_cast<const float*>(&sm.g[tt][pr])[hf] * 0.6931471805599453f;   // A was scaled by log2 e
                 float gg = oo;
                 if (p.z) {
@@ -453,45 +455,35 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
                 from_f(ou.v[e], fmaf(d, lb, sk * gg));
                 const float dr = fmaf(uu, lb, aq) * sigmoid_f<float>(raw);
                 from_f(od.v[e], dr);
-                acc_skip[v][e] = fmaf(gg, uu, acc_skip[v][e]);
-                acc_bias[v][e] += dr;
+                reinterpret_cast<float2*>(&sm.dx[tt][pr])[hf] = make_float2(gg * uu, dr);
             }
             const size_t at = (row + t + tt) * D + c0 + cv * V;
             *reinterpret_cast<Pack<T, V>*>((T*)p.du + at) = ou;
             *reinterpret_cast<Pack<T, V>*>((T*)p.ddt + at) = od;
             if (p.z) *reinterpret_cast<Pack<T, V>*>((T*)p.dz + at) = oz;
         }
-        __syncthreads();
         if constexpr (V > 1) fetch(t - 2 * TL, slot, true);
+        __syncthreads();
+        if (threadIdx.x < CPB) {
+            for (int tt = 0; tt < nt; ++tt) {
+                const float2 e = reinterpret_cast<const float2*>(&sm.dx[tt][0])[threadIdx.x];
+                dskip += e.x;
+                dbias += e.y;
+            }
+        }
+        __syncthreads();
     }
     if constexpr (V > 1) copy_wait<0>();
 #pragma unroll
     for (int c = 0; c < CH; ++c)
         if (live[c])
             *reinterpret_cast<ulonglong2*>(ws.dA + wr * N + cn0[c]) = make_ulonglong2(dA[c][0], dA[c][1]);
-    // dskip, ddt_bias of the chunk: the element lanes' sums, added per channel in a fixed order
-    float* s_a = reinterpret_cast<float*>(&sm.keep[0][0][0]);   // [tile tokens][CPB]: the kept states are done with
-    float* s_b = s_a + TL * CPB;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = v * kBwdThreads + threadIdx.x;
-        if (i >= S::VECS) break;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            s_a[i / CV * CPB + i % CV * V + e] = acc_skip[v][e];
-            s_b[i / CV * CPB + i % CV * V + e] = acc_bias[v][e];
+    if (threadIdx.x < CPB) {
+        const int c = threadIdx.x % S::PV * S::VP + threadIdx.x / S::PV;
+        if (c < cn) {
+            ws.dskip[wr + c0 + c] = dskip;
+            ws.dbias[wr + c0 + c] = dbias;
         }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < cn; c += kBwdThreads) {
-        float sa = 0.f, sb = 0.f;
-#pragma unroll
-        for (int tt = 0; tt < TL; ++tt) {
-            sa += s_a[tt * CPB + c];
-            sb += s_b[tt * CPB + c];
-        }
-        ws.dskip[wr + c0 + c] = sa;
-        ws.dbias[wr + c0 + c] = sb;
     }
 }
 
@@ -520,7 +512,7 @@ __global__ void __launch_bounds__(256) k_bwd_params(ScanArgs p, BwdWs ws, int ro
     const size_t step = i < DN ? DN : D;
     float acc = 0.f;
     if (i < all) {
-#pragma unroll 4
+#pragma unroll 16
         for (int r = y; r < rows; r += 8) acc += src[r * step];
     }
     s[y][lane] = acc;
@@ -536,8 +528,7 @@ __global__ void __launch_bounds__(256) k_bwd_params(ScanArgs p, BwdWs ws, int ro
 template <typename T, int N, int V>
 static void bwd_launch(const SsmHandle& h, const ScanArgs& a, const BwdPlan& pl, const BwdWs& ws, cudaStream_t st) {
     using S = BwdShared<T, N, V>;
-    static_assert(sizeof(float4) * (S::CHUNK / kBwdSub) * kBwdCH * kBwdThreads >= 2 * kBwdTile * S::CPB * sizeof(float),
-                  "the last sums are made where the kept states were");
+    static_assert(S::CPB <= kBwdThreads, "a thread for every channel");
     // the attribute's failure shows as the launch's
     cudaFuncSetAttribute(k_bwd_main<T, N, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S));
     k_bwd_main<T, N, V><<<(unsigned)pl.tiles * a.B * pl.nC, kBwdThreads, sizeof(S), st>>>(a, pl, ws, h.D, h.G);
@@ -556,7 +547,7 @@ favor_status scan_backward(const SsmHandle& h, const ScanArgs& a, cudaStream_t s
     const BwdPlan pl = bwd_plan(h, a.L);
     size_t total = 0;
     const BwdWs ws = bwd_layout(h.ws, pl, a.B, a.L, h.D, h.N, h.G, &total);
-    const bool vec = scan_grad_chunks(h, a, ws.s, bwd_chunk(h), st);
+    const bool vec = scan_grad_chunks(h, a, ws.s, kBwdChunk, st);
     if (f32 && vec) bwd_by_n<float, 4>(h, a, pl, ws, st);
     else if (f32) bwd_by_n<float, 1>(h, a, pl, ws, st);
     else if (vec) bwd_by_n<__nv_bfloat16, 8>(h, a, pl, ws, st);
