@@ -16,10 +16,6 @@
 
 #include "ssm_internal.h"
 
-#ifndef BCH
-#define BCH 32
-#define BMB 3
-#endif
 namespace favor {
 
 constexpr int kBwdThreads = 128;
@@ -27,8 +23,9 @@ constexpr int kBwdSub = 4;          // tokens whose states are in registers at a
 constexpr int kBwdTile = 16;        // tokens staged in shared memory at a time
 constexpr int kBwdNS = 4;           // states a thread, of
 constexpr int kBwdCH = 2;           // channels
-// Tokens of a chunk: the kept states take 8 KB for every 4 of them.
-constexpr int kBwdChunk = BCH;
+// Tokens of a chunk: the kept states take 4 KB for every 4 of them, and three blocks of 75 KB share an
+// SM (64 tokens and two blocks, before the states were formed a channel at a time: 4% slower).
+constexpr int kBwdChunk = 32;
 
 struct BwdPlan {
     int tiles, tpg, Dg, nC;
@@ -117,14 +114,22 @@ struct BwdShared {
     float4 dx[kBwdTile][PAIRS + PAD];
     float2 g[kBwdTile][PAIRS + PAD];
     alignas(16) float bc[2][kBwdTile][N];
-    alignas(16) float red[W][kBwdTile][LPC][8];
+    // dB, dC of 4 tokens from each warp, [token][part][8], go where the warp kept the states before them
+    static constexpr bool ALIAS = LPC * kBwdSub * 8 * sizeof(float) <= sizeof(float4) * 32 * kBwdCH;
+    alignas(16) float red[ALIAS ? 1 : W][ALIAS ? 1 : kBwdTile / kBwdSub][ALIAS ? 4 : kBwdSub * LPC * 8];
+    __device__ __forceinline__ float* part_sums(int warp, int sub, int o) {
+        if constexpr (ALIAS) return reinterpret_cast<float*>(&keep[sub][o >> 7][warp * 32]) + (o & 127);
+        else return &red[warp][sub % (kBwdTile / kBwdSub)][o];
+    }
+    float d[CHUNK][CPB];   // dt of the chunk, a row's places turned by its number against bank conflicts
+    static __device__ __forceinline__ int turned(int tt, int place) { return place ^ ((tt & 3) << 3 & (CPB - 1)); }
     Pack<T, V> raw[2][4][NV][kBwdThreads];
     Pack<T, BV> rawbc[2][2][EB > 1 ? EB * kBwdThreads : BC];
     alignas(16) float sbias[CPB], sskip[CPB];   // by place
 };
 
 template <typename T, int N, int V>
-__global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPlan pl, BwdWs ws, int D, int G) {
+__global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan pl, BwdWs ws, int D, int G) {
     using S = BwdShared<T, N, V>;
     constexpr int NS = kBwdNS, CH = kBwdCH, LPC = S::LPC, CPB = S::CPB, CV = S::CV, NV = S::NV, BV = S::BV, EB = S::EB;
     constexpr int TL = kBwdTile, SUB = kBwdSub;
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
         if constexpr (V > 1) copy_commit();
     };
     // the tile's elements arrive: dt, dt u (and g) for the state lanes, B (and C)
-    auto arrive = [&](int slot, bool back) {
+    auto arrive = [&](int t, int slot, bool back) {
         if constexpr (V > 1) {
             copy_wait<1>();
         } else {
@@ -224,12 +229,17 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             float d[V + V % 2];
             if constexpr (V == 1) d[1] = 0.f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) d[e] = to_f(rd.v[e]) + sm.sbias[S::place(cv * V + e)];
+            for (int e = 0; e < V; ++e)
+                d[e] = back ? sm.d[t - t0 + tt][S::turned(tt, S::place(cv * V + e))]
+                            : to_f(rd.v[e]) + sm.sbias[S::place(cv * V + e)];
+            if (!back) {
 #pragma unroll
-            for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
+                for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
+            }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const int at = S::place(cv * V + e);
+                if (!back) sm.d[t - t0 + tt][S::turned(tt, at)] = d[e];
                 reinterpret_cast<float2*>(&sm.dx[tt][0])[at] = make_float2(d[e], d[e] * to_f(ru.v[e]));
             }
             if (back) {
@@ -291,23 +301,24 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
     int slot = 0;
     for (int t = t0; t < t1; t += TL, slot ^= 1) {
         const int nt = min(TL, t1 - t);
-        arrive(slot, false);
+        arrive(t, slot, false);
         if constexpr (V == 1) fetch_ahead(t + TL, 0);
-        for (int tt = 0; tt < nt; ++tt) {
-            if (tt % SUB == 0) {
+        for (int tt = 0; tt < nt; tt += SUB) {
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    *reinterpret_cast<ulonglong2*>(&sm.keep[(t - t0 + tt) / SUB][c][threadIdx.x]) = make_ulonglong2(h[c][0], h[c][1]);
-            }
-            if (t == last && tt >= (nt - 1) / SUB * SUB) break;   // the states behind are not asked for
-            const float4 d4 = sm.dx[tt][q];
-            const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w};
-            const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt][part * NS]);
+            for (int c = 0; c < CH; ++c)
+                *reinterpret_cast<ulonglong2*>(&sm.keep[(t - t0 + tt) / SUB][c][threadIdx.x]) = make_ulonglong2(h[c][0], h[c][1]);
+            if (t == last && tt + SUB >= nt) break;   // the states behind are not asked for
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]);
-                h[c][0] = fma2(ex2_2(fma2(A2[c][0], d2, mean2)), h[c][0], mul2(x2, bb.x));
-                h[c][1] = fma2(ex2_2(fma2(A2[c][1], d2, mean2)), h[c][1], mul2(x2, bb.y));
+            for (int k = 0; k < SUB; ++k) {
+                const float4 d4 = sm.dx[tt + k][q];
+                const float dd[CH] = {d4.x, d4.z}, xx[CH] = {d4.y, d4.w};
+                const ulonglong2 bb = *reinterpret_cast<const ulonglong2*>(&sm.bc[0][tt + k][part * NS]);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]);
+                    h[c][0] = fma2(ex2_2(fma2(A2[c][0], d2, mean2)), h[c][0], mul2(x2, bb.x));
+                    h[c][1] = fma2(ex2_2(fma2(A2[c][1], d2, mean2)), h[c][1], mul2(x2, bb.y));
+                }
             }
         }
         __syncthreads();
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
 
     for (int t = last; t >= t0; t -= TL, slot ^= 1) {
         const int nt = min(TL, t1 - t);
-        arrive(slot, true);
+        arrive(t, slot, true);
         if constexpr (V == 1) fetch(t - TL, 0, true);
         auto sub = [&](int s0, int ns, auto full) {
             constexpr bool FULL = decltype(full)::value;
@@ -410,11 +421,12 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             if constexpr (LEFTW % 4 == 0) {
 #pragma unroll
                 for (int i = 0; i < LEFTW; i += 4)
-                    *reinterpret_cast<float4*>(&sm.red[warp][s0 + fw / 8 + i / 8][part][fw % 8 + i % 8]) =
+                    *reinterpret_cast<float4*>(sm.part_sums(warp, (t - t0 + s0) / SUB, ((fw / 8 + i / 8) * LPC + part) * 8 + fw % 8 + i % 8)) =
                         make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             } else {
 #pragma unroll
-                for (int i = 0; i < LEFTW; ++i) sm.red[warp][s0 + fw / 8][part][fw % 8 + i] = w[i];
+                for (int i = 0; i < LEFTW; ++i)
+                    *sm.part_sums(warp, (t - t0 + s0) / SUB, (fw / 8 * LPC + part) * 8 + fw % 8 + i) = w[i];
             }
         };
         int s0 = (nt - 1) / SUB * SUB;
@@ -426,9 +438,9 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
         __syncthreads();
         for (int i = threadIdx.x; i < nt * 2 * N; i += kBwdThreads) {
             float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < S::W; ++w) s += (&sm.red[w][0][0][0])[i];
             const int tt = i / (2 * N), j = i % (2 * N);
+#pragma unroll
+            for (int w = 0; w < S::W; ++w) s += *sm.part_sums(w, (t - t0 + tt) / SUB, tt % SUB * 2 * N + j);
             ws.bc[((((size_t)(tile % pl.tpg) * p.B + b) * p.L + t + tt) * G + g) * 2 * N + j] = s;
         }
 #pragma unroll
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
             for (int e = 0; e < V; ++e) {
                 const int at = S::place(cv * V + e), pr = at >> 1, hf = at & 1;
                 const float raw = to_f(rd.v[e]) + sm.sbias[at], sk = sm.sskip[at];
-                const float d = softplus_f(raw), uu = to_f(ru.v[e]), oo = to_f(ro.v[e]);
+                const float d = sm.d[t - t0 + tt][S::turned(tt, at)], uu = to_f(ru.v[e]), oo = to_f(ro.v[e]);
                 const float2 yl = reinterpret_cast<const float2*>(&sm.dx[tt][pr])[hf];
                 const float y = yl.x, lb = yl.y;
                 const float aq = reinterpret_cast<const float*>(&sm.g[tt][pr])[hf] * 0.6931471805599453f;   // A was scaled by log2 e
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(kBwdThreads, BMB) k_bwd_main(ScanArgs p, BwdPl
                     from_f(oz.v[e], oo * fmaf(sk, uu, y) * (sg * (1.f + zz * (1.f - sg))));
                 }
                 from_f(ou.v[e], fmaf(d, lb, sk * gg));
-                const float dr = fmaf(uu, lb, aq) * sigmoid_f<float>(raw);
+                const float dr = fmaf(uu, lb, aq) * sigmoid_f<T>(raw);
                 from_f(od.v[e], dr);
                 reinterpret_cast<float2*>(&sm.dx[tt][pr])[hf] = make_float2(gg * uu, dr);
             }
