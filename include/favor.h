@@ -359,8 +359,8 @@ FAVOR_API favor_status favor_destroy(favor_handle h);
  * zeros in out.  The others read their page, and leave in it the state behind
  * their last token.
  * `lens` is a DEVICE int array [B] or NULL: row b has lens[b] tokens (clamped
- * to [0, L]); rows of out, and of the gradients dx, du, ddt, dz, dB and dC,
- * behind a row's end are neither read nor written.
+ * to [0, L]).  Nothing behind a row's end is read; there out is left as it was,
+ * and the gradients dx, du, ddt, dz, dB and dC are zero.
  *
  * Same rules as for a favor_handle: every call only enqueues work on `stream`,
  * checks run on the host before any launch, a handle belongs to the device that
@@ -376,7 +376,7 @@ typedef struct favor_ssm_s* favor_ssm;
  * favor_ssm_create -- a handle for D channels, N states, G groups, K taps.
  * Supported: N in {8, 16, 32, 64}, K in {2, 3, 4} (else FAVOR_ERR_UNSUPPORTED);
  * D a multiple of G, of any size up to 2^20; max_B*max_L up to 2^30;
- * max_B*max_L*D, max_B*max_L*G*N and max_B*D*N up to 2^36.  training != 0 allocates the backward calls'
+ * max_B*D up to 2^30; max_B*max_L*D, max_B*max_L*G*N and max_B*D*N up to 2^36.  training != 0 allocates the backward calls'
  * workspace (8*N*G bytes a token for every 512 / N channels of a group, and
  * 12*N*D bytes for every 128 tokens of a row); without it they give
  * FAVOR_ERR_UNSUPPORTED.

@@ -192,6 +192,8 @@ k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
     const T* x = (const T*)a.x + (size_t)b * a.L * D + c;
     const T* dout = (const T*)a.dout + (size_t)b * a.L * D + c;
     T* dx = (T*)a.dx + (size_t)b * a.L * D + c;
+    for (int t = max(t0, len); t < min(t0 + R, a.L); ++t)   // behind the row's end: no gradient
+        *reinterpret_cast<Pack<T, V>*>(dx + (size_t)t * D) = zero_pack<T, V>();
     float w[V][K], bias[V];
     load_taps<V, K>(a.weight, a.bias, c, w, bias);
     float xs[V][K], gs[V][K], dw[V][K], db[V];   // xs: x[t-K+1 .. t]; gs: g[t-K+1 .. t]

@@ -206,6 +206,8 @@ static bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+static bool int_aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
 static favor_status check_pool(const char* fn, const void* pool, int n_pages, size_t page_bytes) {
     if (!pool) return set_error(FAVOR_ERR_INVALID_ARG, "%s: null pool", fn);
     if (n_pages < 1 || page_bytes < 1)
@@ -246,6 +248,13 @@ favor_status favor_pages_copy(void* dst_pool, int n_dst, const void* src_pool, i
     if (st != FAVOR_OK) return st;
     if (!src || !dst) return set_error(FAVOR_ERR_INVALID_ARG, "%s: null index pointer", fn);
     if (n < 1) return set_error(FAVOR_ERR_INVALID_ARG, "%s: n=%d must be >= 1", fn, n);
+    if (!int_aligned(src) || !int_aligned(dst) || !int_aligned(done))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: an index pointer is not aligned", fn);
+    const size_t ib = (size_t)n * 4, db = (size_t)n_dst * page_bytes;
+    if (ranges_overlap(src, ib, dst_pool, db) || ranges_overlap(dst, ib, dst_pool, db) ||
+        (done && (ranges_overlap(done, ib, dst_pool, db) || ranges_overlap(done, ib, src, ib) ||
+                  ranges_overlap(done, ib, dst, ib) || ranges_overlap(done, ib, src_pool, (size_t)n_src * page_bytes))))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: the indices, done and the pools must not overlap", fn);
     if (dst_pool != src_pool &&
         ranges_overlap(dst_pool, (size_t)n_dst * page_bytes, src_pool, (size_t)n_src * page_bytes))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: the pools overlap without being the same", fn);
@@ -267,6 +276,9 @@ favor_status favor_pages_clear(void* pool, int n_pages, size_t page_bytes, const
     if (st != FAVOR_OK) return st;
     if (!pages) return set_error(FAVOR_ERR_INVALID_ARG, "%s: null index pointer", fn);
     if (n < 1) return set_error(FAVOR_ERR_INVALID_ARG, "%s: n=%d must be >= 1", fn, n);
+    if (!int_aligned(pages)) return set_error(FAVOR_ERR_INVALID_ARG, "%s: an index pointer is not aligned", fn);
+    if (ranges_overlap(pages, (size_t)n * 4, pool, (size_t)n_pages * page_bytes))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: the indices and the pool must not overlap", fn);
     const int wb = word_bytes(pool, pool, page_bytes);
     int slices = 0;
     const unsigned grid = page_grid(n, page_bytes / wb, &slices);
@@ -288,7 +300,12 @@ favor_status favor_pages_compact(void* pool, int n_pages, size_t page_bytes, con
     if (S < 1) return set_error(FAVOR_ERR_INVALID_ARG, "%s: S=%d must be >= 1", fn, S);
     if (n_pages > kMaxPages)
         return set_error(FAVOR_ERR_UNSUPPORTED, "%s: n_pages=%d (at most %d)", fn, n_pages, kMaxPages);
-    const size_t tb = (size_t)S * 4;
+    if (!int_aligned(table) || !int_aligned(new_table) || !int_aligned(page_map) || !int_aligned(n_live))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: an index pointer is not aligned", fn);
+    const size_t tb = (size_t)S * 4, pb = (size_t)n_pages * page_bytes;
+    if (ranges_overlap(table, tb, pool, pb) || ranges_overlap(new_table, tb, pool, pb) ||
+        ranges_overlap(n_live, 4, pool, pb) || (page_map && ranges_overlap(page_map, (size_t)n_pages * 4, pool, pb)))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: the tables and the pool must not overlap", fn);
     if (ranges_overlap(table, tb, new_table, tb) || ranges_overlap(table, tb, n_live, 4) ||
         ranges_overlap(new_table, tb, n_live, 4) ||
         (page_map && (ranges_overlap(table, tb, page_map, (size_t)n_pages * 4) ||
@@ -321,6 +338,9 @@ favor_status favor_pages_move(void* pool, int n_pages, size_t page_bytes, const 
     favor_status st = check_pool(fn, pool, n_pages, page_bytes);
     if (st != FAVOR_OK) return st;
     if (!page_map) return set_error(FAVOR_ERR_INVALID_ARG, "%s: null page_map", fn);
+    if (!int_aligned(page_map)) return set_error(FAVOR_ERR_INVALID_ARG, "%s: an index pointer is not aligned", fn);
+    if (ranges_overlap(page_map, (size_t)n_pages * 4, pool, (size_t)n_pages * page_bytes))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: the map and the pool must not overlap", fn);
     const int wb = word_bytes(pool, pool, page_bytes);
     int slices = 0;
     const unsigned grid = page_grid(n_pages, page_bytes / wb, &slices);

@@ -50,8 +50,8 @@ struct ScanPlan {
 // A tile passes through three steps: every thread turns 8 elements (token,
 // channel) into dt and dt u in shared memory; the state lanes walk the tile's
 // tokens and leave y there; every thread turns its elements' y into outputs.  The
-// elements come by 16-byte asynchronous copies, two tiles deep, each thread
-// copying what it alone reads (no barrier between them); rows that do not start on 16
+// elements come by asynchronous copies, two tiles deep, each thread
+// copying what it alone reads (no barrier between them); 16-bit rows that do not start on 16
 // bytes go through registers one tile ahead.
 // Channel cl of a tile sits at place (cl % V) CV + cl / V of a shared row, so
 // that the V channels of a thread's access land V different rows' width apart
@@ -62,6 +62,7 @@ struct ScanShared {
     static constexpr int LPC = N / kScanNS, CPB = kScanThreads * kScanCH / LPC;
     static constexpr int EPT = V > 1 ? 32 / (int)sizeof(T) : 8;        // elements a thread, two copies of 16 bytes
     static constexpr int TT = EPT * kScanThreads / CPB, NV = EPT / V, CV = CPB / V;
+    static constexpr bool ASYNC = sizeof(Pack<T, V>) >= 4;             // asynchronous copies move 4 bytes at least
     static constexpr int NT = MODE == SCAN_OUT ? 3 : MODE == SCAN_SUM ? 2 : 4;   // u, dt, z, dout
     static constexpr int NM = MODE == SCAN_SUM ? 1 : 2;                // B, C
     static constexpr int BV = V > 1 ? 16 / (int)sizeof(T) : 1;         // elements of B and C a copy
@@ -119,8 +120,8 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         ev_c[v] = i % CV;
     }
     // registers of the narrow path, one tile ahead of the shared slots
-    Pack<T, V> rr[V == 1 ? S::NT : 1][V == 1 ? NV : 1];
-    T rbc[V == 1 ? S::NM : 1][V == 1 ? EB : 1];
+    Pack<T, V> rr[S::ASYNC ? 1 : S::NT][S::ASYNC ? 1 : NV];
+    T rbc[S::ASYNC ? 1 : S::NM][S::ASYNC ? 1 : EB];
     auto fetch = [&](int t, int slot) {
         const T* src[4] = {u, dt, z, dout};
 #pragma unroll
@@ -129,7 +130,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
             for (int v = 0; v < NV; ++v) {
                 const bool ok = t + ev_t[v] < t1 && ev_c[v] * V < cn && (k != 2 || z);
                 const T* at = ok ? src[k] + (size_t)(t + ev_t[v]) * D + ev_c[v] * V : u;
-                if constexpr (V > 1) {
+                if constexpr (S::ASYNC) {
                     copy_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
                 } else {
                     rr[k][v] = ok ? load_pack<T, V>(at) : zero_pack<T, V>();
@@ -143,18 +144,18 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 const int e = i * kScanThreads + threadIdx.x, tt = e / (N / BV), n = e % (N / BV) * BV;
                 const bool ok = e < BC && t + tt < t1;
                 const T* at = ok ? mat[k] + (size_t)(t + tt) * G * N + n : mat[k];
-                if constexpr (V > 1) {
+                if constexpr (S::ASYNC) {
                     if (e < BC) copy_async(&sm.rawbc[slot][k][i][threadIdx.x], at, ok);
                 } else {
                     from_f(rbc[k][i], 0.f);
                     if (ok) rbc[k][i] = *at;
                 }
             }
-        if constexpr (V > 1) copy_commit();
+        if constexpr (S::ASYNC) copy_commit();
     };
     // the tile's elements are in this thread's slots
     auto arrive = [&](int slot) {
-        if constexpr (V > 1) {
+        if constexpr (S::ASYNC) {
             copy_wait<1>();
         } else {
 #pragma unroll
@@ -168,7 +169,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
         }
     };
     fetch(t0, 0);
-    if constexpr (V > 1) fetch(t0 + TT, 1);
+    if constexpr (S::ASYNC) fetch(t0 + TT, 1);
 
     // state lanes: the channels at places 2q and 2q + 1, states part*8 .. +7
     const int q = threadIdx.x / LPC, part = threadIdx.x % LPC;
@@ -364,7 +365,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 }
             }
         __syncthreads();
-        if constexpr (V == 1) fetch(t + TT, 0);
+        if constexpr (!S::ASYNC) fetch(t + TT, 0);
         int tt = 0;
         for (; tt + UN <= nt; tt += UN) {
             if (GRAD && t + tt == t0 + (chunk - rest / p.B * pl.per + 1) * pl.Lc) next_chunk();
@@ -403,9 +404,9 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 *reinterpret_cast<Pack<T, V>*>(out + (size_t)(t + ev_t[v]) * D + ev_c[v] * V) = o;
             }
         }
-        if constexpr (V > 1) fetch(t + 2 * TT, slot);
+        if constexpr (S::ASYNC) fetch(t + 2 * TT, slot);
     }
-    if constexpr (V > 1) copy_wait<0>();
+    if constexpr (S::ASYNC) copy_wait<0>();
     leave();
 }
 

@@ -105,6 +105,7 @@ struct BwdShared {
     // forward kernel; the narrow path keeps the places, and with them the order of the sums.
     static constexpr int VP = 16 / (int)sizeof(T), PV = CPB / VP;
     static __device__ __forceinline__ int place(int cl) { return cl % VP * PV + cl / VP; }
+    static constexpr bool ASYNC = sizeof(Pack<T, V>) >= 4;   // asynchronous copies move 4 bytes at least
     static constexpr int VECS = kBwdTile * CV, NV = (VECS + kBwdThreads - 1) / kBwdThreads;
     static constexpr int BV = V > 1 ? 16 / (int)sizeof(T) : 1;
     static constexpr int BC = kBwdTile * N / BV, EB = (BC + kBwdThreads - 1) / kBwdThreads;
@@ -155,7 +156,15 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
         if (!live[c]) ch[c] = 0;
         cn0[c] = (size_t)(c0 + ch[c]) * N + part * NS;
     }
-    if (t0 >= t1) {   // behind the row's end: zeros for the sums over rows
+    // rows of the chunk behind the row's end: no gradient
+    const int tz = max(t0, t1), nz = min(t0 + S::CHUNK, p.L) - tz;
+    for (int i = threadIdx.x; i < nz * cn; i += kBwdThreads) {
+        const size_t at = (row + tz + i / cn) * D + c0 + i % cn;
+        from_f(((T*)p.du)[at], 0.f);
+        from_f(((T*)p.ddt)[at], 0.f);
+        if (p.z) from_f(((T*)p.dz)[at], 0.f);
+    }
+    if (t0 >= t1) {   // and zeros for the sums over rows
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             if (!live[c]) continue;
@@ -166,8 +175,8 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
     }
     const T* src[4] = {(const T*)p.u, (const T*)p.dt, (const T*)p.z, (const T*)p.dout};
     const T* mat[2] = {(const T*)p.Bm + (row * G + g) * N, (const T*)p.Cm + (row * G + g) * N};
-    Pack<T, V> rr[4][V == 1 ? NV : 1];
-    T rbc[2][V == 1 ? EB : 1];
+    Pack<T, V> rr[4][S::ASYNC ? 1 : NV];
+    T rbc[2][S::ASYNC ? 1 : EB];
     // tile at t: nk = 2 tensors (forwards: u, dt, B) or 4 (backwards)
     auto fetch = [&](int t, int slot, bool back) {
 #pragma unroll
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
                 const int i = v * kBwdThreads + threadIdx.x, tt = i / CV, c = i % CV * V;
                 const bool ok = i < S::VECS && t >= t0 && t + tt < t1 && c < cn && (k != 2 || p.z);
                 const T* at = ok ? src[k] + (row + t + tt) * D + c0 + c : src[0];
-                if constexpr (V > 1) copy_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
+                if constexpr (S::ASYNC) copy_async(&sm.raw[slot][k][v][threadIdx.x], at, ok);
                 else rr[k][v] = ok ? load_pack<T, V>(at) : zero_pack<T, V>();
             }
         }
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
                 const int e = i * kBwdThreads + threadIdx.x, tt = e / (N / BV), n = e % (N / BV) * BV;
                 const bool ok = e < S::BC && t >= t0 && t + tt < t1;
                 const T* at = ok ? mat[k] + (size_t)(t + tt) * G * N + n : mat[k];
-                if constexpr (V > 1) {
+                if constexpr (S::ASYNC) {
                     if (e < S::BC) copy_async(&sm.rawbc[slot][k][e], at, ok);
                 } else {
                     from_f(rbc[k][i], 0.f);
@@ -198,11 +207,11 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
                 }
             }
         }
-        if constexpr (V > 1) copy_commit();
+        if constexpr (S::ASYNC) copy_commit();
     };
     // the tile's elements arrive: dt, dt u (and g) for the state lanes, B (and C)
     auto arrive = [&](int t, int slot, bool back) {
-        if constexpr (V > 1) {
+        if constexpr (S::ASYNC) {
             copy_wait<1>();
         } else {
 #pragma unroll
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
         sm.sskip[S::place(c)] = c < cn && p.skip ? p.skip[c0 + c] : 0.f;
     }
     fetch_ahead(t0, 0);
-    if constexpr (V > 1) fetch_ahead(t0 + TL, 1);
+    if constexpr (S::ASYNC) fetch_ahead(t0 + TL, 1);
     // states of a thread as packed pairs; a place without a channel stays zero throughout
     uint64_t A2[CH][2], h[CH][2], mu[CH][2], dA[CH][2];
     const uint64_t mean2 = pack2(kEx2Mean, kEx2Mean);
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
     for (int t = t0; t < t1; t += TL, slot ^= 1) {
         const int nt = min(TL, t1 - t);
         arrive(t, slot, false);
-        if constexpr (V == 1) fetch_ahead(t + TL, 0);
+        if constexpr (!S::ASYNC) fetch_ahead(t + TL, 0);
         for (int tt = 0; tt < nt; tt += SUB) {
 #pragma unroll
             for (int c = 0; c < CH; ++c)
@@ -322,7 +331,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
             }
         }
         __syncthreads();
-        if constexpr (V > 1) fetch_ahead(t + 2 * TL, slot);
+        if constexpr (S::ASYNC) fetch_ahead(t + 2 * TL, slot);
     }
     // backwards
     float dskip = 0.f, dbias = 0.f;   // of the channel at place threadIdx.x
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
     for (int t = last; t >= t0; t -= TL, slot ^= 1) {
         const int nt = min(TL, t1 - t);
         arrive(t, slot, true);
-        if constexpr (V == 1) fetch(t - TL, 0, true);
+        if constexpr (!S::ASYNC) fetch(t - TL, 0, true);
         auto sub = [&](int s0, int ns, auto full) {
             constexpr bool FULL = decltype(full)::value;
             uint64_t accB[SUB][2], accC[SUB][2];
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
             *reinterpret_cast<Pack<T, V>*>((T*)p.ddt + at) = od;
             if (p.z) *reinterpret_cast<Pack<T, V>*>((T*)p.dz + at) = oz;
         }
-        if constexpr (V > 1) fetch(t - 2 * TL, slot, true);
+        if constexpr (S::ASYNC) fetch(t - 2 * TL, slot, true);
         __syncthreads();
         if (threadIdx.x < CPB) {
             for (int tt = 0; tt < nt; ++tt) {
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
         }
         __syncthreads();
     }
-    if constexpr (V > 1) copy_wait<0>();
+    if constexpr (S::ASYNC) copy_wait<0>();
 #pragma unroll
     for (int c = 0; c < CH; ++c)
         if (live[c])
@@ -499,18 +508,18 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
     }
 }
 
-// dB, dC: the channel tiles' parts, in order, rounded once.  Rows behind a
-// sequence's end are left as they were.
+// dB, dC: the channel tiles' parts, in order, rounded once; zero behind a row's end.
 template <typename T>
 __global__ void __launch_bounds__(256) k_bwd_bc(ScanArgs p, BwdPlan pl, BwdWs ws, int N, int G) {
     const size_t n = (size_t)p.B * p.L * G * 2 * N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const size_t tg = i / (2 * N);
     const int j = (int)(i % (2 * N)), t = (int)(tg / G % p.L), b = (int)(tg / G / p.L);
-    if (t >= row_len(p.lens, b, p.L)) return;
     float s = 0.f;
+    if (t < row_len(p.lens, b, p.L)) {
 #pragma unroll 8
-    for (int k = 0; k < pl.tpg; ++k) s += ws.bc[k * n + i];
+        for (int k = 0; k < pl.tpg; ++k) s += ws.bc[k * n + i];
+    }
     T* o = (T*)(j & 4 ? p.dC : p.dB) + tg * N + j / 8 * 4 + (j & 3);
     from_f(*o, s);
 }

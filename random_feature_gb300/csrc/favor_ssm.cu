@@ -1,6 +1,7 @@
 // Host side of the selective scan and the short causal convolution: argument
 // checks, handle lifetime, workspace.  Every check runs before anything is
 // enqueued; a failing call launches nothing.
+#include <initializer_list>
 #include <new>
 
 #include "ssm_internal.h"
@@ -66,7 +67,14 @@ favor_status check_pages(const char* fn, const void* pool, const int* pages, int
     return FAVOR_OK;
 }
 
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// Whether every tensor starts on an element of it.
+bool aligned(size_t es, std::initializer_list<const void*> tensors, std::initializer_list<const void*> words) {
+    for (const void* p : tensors)
+        if (reinterpret_cast<uintptr_t>(p) % es) return false;
+    for (const void* p : words)
+        if (reinterpret_cast<uintptr_t>(p) % 4) return false;
+    return true;
+}
 
 }  // namespace
 
@@ -89,8 +97,8 @@ favor_status favor_ssm_create(favor_ssm* out, int D, int N, int G, int K, favor_
     if (K < 2 || K > 4) return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: K=%d (supported: 2, 3, 4)", K);
     if (D > (1 << 20) || (long long)max_B * max_L > (1LL << 30) || (long long)max_B * max_L > (1LL << 36) / D)
         return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: D or max_B*max_L*D too large");
-    if ((long long)max_B * N > (1LL << 36) / D || (long long)max_B * max_L * N > (1LL << 36) / G)
-        return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: max_B*D*N or max_B*max_L*G*N too large");
+    if ((long long)max_B * D > (1LL << 30) || (long long)max_B * N > (1LL << 36) / D || (long long)max_B * max_L * N > (1LL << 36) / G)
+        return set_error(FAVOR_ERR_UNSUPPORTED, "favor_ssm_create: max_B*D, max_B*D*N or max_B*max_L*G*N too large");
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
@@ -146,7 +154,7 @@ static favor_status conv_call(const char* fn, favor_ssm hd, const void* x, const
     const size_t es = esize(h), page = (size_t)(h.K - 1) * h.D * es, n = (size_t)B * L * h.D * es;
     st = check_pages(fn, window, pages, n_pages, B, page, step);
     if (st != FAVOR_OK) return st;
-    if (!aligned(x, es) || !aligned(out, es) || !aligned(window, es))
+    if (!aligned(es, {x, out, window}, {weight, bias, pages, lens}))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", fn);
     const Span outs[] = {{out, n}, {window, window ? page * n_pages : 0}};
     const Span ins[] = {{x, n}, {weight, (size_t)h.D * h.K * 4}, {bias, (size_t)h.D * 4},
@@ -182,7 +190,7 @@ favor_status favor_conv_causal_backward(favor_ssm hd, const void* x, const float
     if (!x || !weight || !dout || !dx || !dweight) return set_error(FAVOR_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (!h.training) return set_error(FAVOR_ERR_UNSUPPORTED, "%s: the handle was created without training", fn);
     const size_t es = esize(h), n = (size_t)B * L * h.D * es;
-    if (!aligned(x, es) || !aligned(dout, es) || !aligned(dx, es))
+    if (!aligned(es, {x, dout, dx}, {weight, bias, lens, dweight, dbias}))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", fn);
     const Span outs[] = {{dx, n}, {dweight, (size_t)h.D * h.K * 4}, {dbias, (size_t)h.D * 4}};
     const Span ins[] = {{x, n}, {dout, n}, {weight, (size_t)h.D * h.K * 4}, {bias, (size_t)h.D * 4},
@@ -207,8 +215,7 @@ static favor_status scan_call(const char* fn, favor_ssm hd, const ScanArgs& a, b
     if (st != FAVOR_OK) return st;
     if (a.state && !is_aligned16(a.state))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: state must be 16-byte aligned", fn);
-    if (!aligned(a.u, es) || !aligned(a.dt, es) || !aligned(a.Bm, es) || !aligned(a.Cm, es) || !aligned(a.z, es) ||
-        !aligned(a.out, es))
+    if (!aligned(es, {a.u, a.dt, a.Bm, a.Cm, a.z, a.out}, {a.A, a.skip, a.dt_bias, a.pg.pages, a.lens}))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", fn);
     const Span outs[] = {{a.out, n}, {a.state, a.state ? page * a.pg.n_pages : 0}};
     const Span ins[] = {{a.u, n}, {a.dt, n}, {a.z, n}, {a.Bm, nb}, {a.Cm, nb}, {a.A, page},
@@ -255,10 +262,8 @@ favor_status favor_ssm_scan_backward(favor_ssm hd, const void* u, const void* dt
     const Span outs[] = {{du, n}, {ddt, n}, {dz, n}, {dB, nb}, {dC, nb}, {dA, pa}, {dskip, pd}, {ddt_bias, pd}};
     const Span ins[] = {{u, n}, {dt, n}, {z, n}, {dout, n}, {Bm, nb}, {Cm, nb}, {A, pa}, {skip, pd}, {dt_bias, pd},
                         {lens, (size_t)B * 4}};
-    for (const Span& s : outs)
-        if (!aligned(s.p, es)) return set_error(FAVOR_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", fn);
-    for (const Span& s : ins)
-        if (!aligned(s.p, es)) return set_error(FAVOR_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", fn);
+    if (!aligned(es, {u, dt, z, dout, Bm, Cm, du, ddt, dz, dB, dC}, {A, skip, dt_bias, lens, dA, dskip, ddt_bias}))
+        return set_error(FAVOR_ERR_INVALID_ARG, "%s: a pointer is not aligned to its element", fn);
     if (any_overlap(outs, 8, ins, 10))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: the gradients must not overlap another argument", fn);
     ScanArgs a = {};

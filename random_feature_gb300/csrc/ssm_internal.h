@@ -199,7 +199,8 @@ __device__ __forceinline__ float sigmoid_f(float x) {
     if (sizeof(T) == 2) return rcp_approx(1.f + e);
     constexpr float lo = 1.925963033500e-8f;   // log2 e - kLog2e
     const float r = fmaf(-x, lo, fmaf(-x, kLog2e, -t));
-    e = fminf(fmaf(e, r * 0.6931471805599453f, e), 1e38f);
+    if (fabsf(x) < 100.f) e = fmaf(e, r * 0.6931471805599453f, e);   // not of infinities
+    e = fminf(e, 1e38f);
     const float d = 1.f + e, s = rcp_approx(d);
     return fmaf(s, fmaf(-d, s, 1.f), s);
 }

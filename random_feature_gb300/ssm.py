@@ -208,7 +208,7 @@ class Ssm:
         B, L = lead = self._lead(x, 3, "x")
         self._conv_args(lead, x, weight, bias, None, None, lens)
         self._check_all(((dout, _kind(x), "dout"),))
-        dx = self._out(x, None, lens)
+        dx = torch.empty_like(x)
         dweight = torch.empty_like(weight)
         dbias = None if bias is None else torch.empty_like(bias)
         _check(self._lib.favor_conv_causal_backward(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
@@ -260,7 +260,7 @@ class Ssm:
         B, L = lead = self._lead(u, 3, "u")
         self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, None, None, lens)
         self._check_all(((dout, _kind(u), "dout"),))
-        new = torch.empty_like if lens is None else torch.zeros_like
+        new = torch.empty_like
         gr = dict(du=new(u), ddt=new(dt), dA=torch.empty_like(A), dB=new(Bm), dC=new(Cm),
                   dskip=None if skip is None else torch.empty_like(skip), dz=None if z is None else new(z),
                   ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias))

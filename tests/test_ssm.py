@@ -182,6 +182,43 @@ def test_nan_behind_a_row_stays_there():
         assert_within(to_host(dw), ww, "f32")
 
 
+def test_gradients_are_written_whole():
+    """Through the C names into buffers full of NaN: behind a row's end the gradients are zero."""
+    B, L, D, N = 3, 70, 24, 16
+    lens = [70, 0, 33]
+    s = scan_inputs(B, L, D, N, 1, "f32", 29)
+    d = dev(s, "f32")
+    g = to_dev(np.random.default_rng(30).standard_normal((B, L, D)), "f32")
+    w = to_dev(np.random.default_rng(31).standard_normal((D, 4)), "f32")
+    nan = lambda t: torch.full_like(t, float("nan"))
+    with R.Ssm(D, N, 1, 4, "f32", B, L) as f:
+        li = ints(lens)
+        want = f.scan_backward(*(d[k] for k in ("u", "raw", "A", "Bm", "Cm")), g, skip=d["skip"], z=d["z"],
+                               dt_bias=d["dt_bias"], lens=li)
+        got = {k: nan(v) for k, v in want.items()}
+        R.favor_ssm_scan_backward(f.handle, d["u"], d["raw"], d["A"], d["Bm"], d["Cm"], d["skip"], d["z"], d["dt_bias"],
+                                  li, g, *got.values(), B, L)
+        dx, dw = nan(d["u"]), nan(w)
+        R.favor_conv_causal_backward(f.handle, d["u"], w, None, 1, li, g, dx, dw, None, B, L)
+    for k, v in got.items():
+        assert torch.equal(v, want[k]), k
+    for b, n in enumerate(lens):
+        for t in (dx, *(got[k] for k in ("du", "ddt", "dB", "dC", "dz"))):
+            assert (t[b, n:] == 0).all() and torch.isfinite(t[b, :n]).all()
+
+
+def test_infinite_gates():
+    """Gates of either infinity: z sigmoid(z) is infinite above and has no value below, as its parts say."""
+    s = scan_inputs(1, 4, 8, 8, 1, "f32", 32)
+    for dtype in ("f32", "bf16"):
+        d = dev(s, dtype)
+        d["z"][0, 1] = float("inf")
+        d["z"][0, 2] = float("-inf")
+        with R.Ssm(8, 8, 1, 4, dtype, 1, 4) as f:
+            out = to_host(call_scan(f, d))
+        assert np.isinf(out[0, 1]).all() and np.isnan(out[0, 2]).all() and np.isfinite(out[0, [0, 3]]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("case", SCANS, ids=_id)
 def test_scan_backward(case, dtype):

@@ -19,6 +19,7 @@ def _built_library():
     (dict(D=0), BAD), (dict(N=0), BAD), (dict(G=0), BAD), (dict(K=0), BAD), (dict(max_B=0), BAD), (dict(max_L=0), BAD),
     (dict(dtype=2), BAD), (dict(G=3), BAD), (dict(N=12), UNS), (dict(N=128), UNS), (dict(K=1), UNS), (dict(K=5), UNS),
     (dict(D=1 << 21), UNS), (dict(max_B=1 << 16, max_L=1 << 15), UNS), (dict(D=1 << 20, max_L=1 << 20), UNS),
+    (dict(D=1 << 20, max_B=1 << 11, max_L=1), UNS), (dict(D=1 << 16, G=1 << 16, max_B=8, max_L=1 << 14), UNS),
 ])
 def test_create_refuses(kw, want):
     a = {**dict(D=64, N=16, G=1, K=4, dtype=0, max_B=2, max_L=128), **kw}
@@ -61,6 +62,15 @@ MB = 1 << 20
     (lambda L: L.favor_pages_compact(MB, 4, 16, 64, 3, 72, None, 128, None), BAD),        # table and new_table overlap
     (lambda L: L.favor_pages_compact(MB, 4, 16, 64, 3, 96, 100, 128, None), BAD),         # new_table and page_map
     (lambda L: L.favor_pages_compact(MB, (1 << 17) + 1, 16, 4, 1, 64, None, 128, None), UNS),
+    (lambda L: L.favor_pages_copy(MB, 4, 2 * MB, 4, 16, 6, 4, 1, None, None), BAD),       # index off its element
+    (lambda L: L.favor_pages_copy(MB, 4, 2 * MB, 4, 16, MB + 8, 4, 1, None, None), BAD),  # indices in the pool
+    (lambda L: L.favor_pages_copy(MB, 4, 2 * MB, 4, 16, 64, 128, 2, 132, None), BAD),     # done over dst
+    (lambda L: L.favor_pages_clear(MB, 4, 16, MB + 4, 1, None), BAD),
+    (lambda L: L.favor_pages_clear(MB, 4, 16, 5, 1, None), BAD),
+    (lambda L: L.favor_pages_compact(MB, 4, 16, MB, 1, 64, None, 128, None), BAD),
+    (lambda L: L.favor_pages_compact(MB, 4, 16, 6, 1, 64, None, 128, None), BAD),
+    (lambda L: L.favor_pages_move(MB, 4, 16, MB + 4, None), BAD),
+    (lambda L: L.favor_pages_move(MB, 4, 16, 7, None), BAD),
     (lambda L: L.favor_pages_move(None, 4, 16, 4, None), BAD),
     (lambda L: L.favor_pages_move(MB, 4, 16, None, None), BAD),
 ])
@@ -111,4 +121,14 @@ def test_calls_refuse():
         with pytest.raises(R.FavorError) as e:      # the state's pages are read 16 bytes at a time
             R.favor_ssm_scan(f.handle, u, u, A, bc, bc, None, None, None, st.data_ptr() + 4, None, B, None,
                              torch.empty_like(u), B, L)
-        assert e.value.status == BAD and R.favor_launch_count() == n0
+        assert e.value.status == BAD
+        off = A.data_ptr() + 2                      # parameters and tensors start on their elements
+        for call in (lambda: R.favor_ssm_scan(f.handle, u, u, off, bc, bc, None, None, None, None, None, 0, None,
+                                              torch.empty_like(u), B, L),
+                     lambda: R.favor_conv_causal(f.handle, u, off, None, 1, None, None, 0, None, torch.empty_like(u), B, L),
+                     lambda: R.favor_conv_causal(f.handle, u.data_ptr() + 1, w, None, 1, None, None, 0, None,
+                                                 torch.empty_like(u), B, L, stream=0)):
+            with pytest.raises(R.FavorError) as e:
+                call()
+            assert e.value.status == BAD and "aligned" in str(e.value)
+        assert R.favor_launch_count() == n0
