@@ -18,17 +18,18 @@ enum { SCAN_OUT, SCAN_SUM, SCAN_GRAD };
 // channels of one group of one row, for one chunk of tokens walked in tiles of
 // TT.  A thread holds 8 states of 2 channels, LPC = N / 8 lanes a channel pair.
 //
-// What bounds it: at N = 16 a token of 32 channels (one warp's) takes 64 packed
-// FMAs and MULs' worth of register reads.  On this device an instruction reads
-// two 32-bit operand words a clock: fma.f32x2 of three distinct operands issues
-// every 3.1 clocks, of two every 2.2, mul.f32x2 every 2.1 (a plain fma: 1.5), so
-// the 32 of a token take 85 clocks of a quarter SM, beside 80 of exponentials
-// (ex2: one in 4) and 115 issue slots.  Measured with full waves: 150 clocks, 4.1
-// ns a thousand (token, channel) pairs; taking out the exponentials, or the
-// loads of B and C, changes that by 1 and 4%.  Two channels a thread share the
-// B and C that every lane loads (one channel a thread: 344 us against 328 at
-// [16, 512, 8192]); a next token's decays formed between this one's updates:
-// 342 us; 5 blocks an SM in 102 registers: 342 us.
+// What bounds it: at N = 16 a token of 32 channels (one warp's) takes 115
+// instructions, 32 of them packed FMAs and MULs and 20 of the exponential unit.  On
+// this device an instruction's operands come from the registers two 32-bit words a
+// clock (measured: fma.f32x2 of three distinct operands issues every 3.1 clocks, of
+// two every 2.2, mul.f32x2 every 2.1, a plain fma 1.5, ex2 every 4.0), so the packed
+// ones take 85 clocks of a quarter SM, the exponentials 80, the issue 115; they
+// overlap in part.  Measured with full waves: 150 clocks.  At [16, 512, 8192], us:
+// 328 so; without the exponentials 324, without the loads of B and C 314, without dt's
+// and the gate's functions 287 (they stood in a copy); one channel a thread, whose
+// lanes do not share the loads of B and C, 344; a token's decays formed between the
+// updates of the one before, 342; 5 blocks an SM in 102 registers, 342; 3 in 168,
+// 367; plain FMAs, 366.  Tokens a step of the walk: 8 against 4 is 2% faster.
 constexpr int kScanNS = 8, kScanCH = 2, kScanPerSm = 4;
 
 struct ScanPlan {
@@ -84,7 +85,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     constexpr int LPC = S::LPC, CPB = S::CPB, TT = S::TT, NV = S::NV, CV = S::CV, BV = S::BV, BC = S::BC, EB = S::EB;
     constexpr int NS = kScanNS, CH = kScanCH;
     constexpr int GK = LPC < 2 ? 1 : LPC / 2;   // tokens whose y are summed over the lanes together: LPC values
-    constexpr int UN = GK < 4 ? 4 : GK;         // tokens a step of the walk
+    constexpr int UN = TT < 8 ? TT : 8;         // tokens a step of the walk, a multiple of GK
     extern __shared__ __align__(16) unsigned char smem[];
     S& sm = *reinterpret_cast<S*>(smem);
 
@@ -558,8 +559,9 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanArgs p, int D, i
 // Cutting the tokens into chunks fills the SMs, but runs every exponential of all
 // but the last chunk twice: with room for 3 chunks or more it pays (1024 tokens,
 // 192 blocks of channels: 205 us in 3 chunks, 227 uncut), with 2 it does not
-// (256 blocks: 271 and 227 us).  A chunk is 64 tokens at least.
-constexpr int kScanMinChunk = 64;
+// (256 blocks: 271 and 227 us).  A chunk is 32 tokens at least (12 blocks of 1000
+// tokens: 26 us, 34 with 64).
+constexpr int kScanMinChunk = 32;
 
 static ScanPlan scan_plan(const SsmHandle& h, int B, int L, int CPB, int TT) {
     ScanPlan pl;
