@@ -105,7 +105,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
     T* out = OUT ? (T*)p.out + row * D + c0 : nullptr;
     if (page < 0) {   // the row takes no part
         if (OUT)
-            for (int i = threadIdx.x; i < (t1 - t0) * cn; i += kScanThreads)
+            for (long long i = threadIdx.x; i < (long long)(t1 - t0) * cn; i += kScanThreads)
                 from_f(out[(size_t)(t0 + i / cn) * D + i % cn], 0.f);
         return;
     }

@@ -342,7 +342,7 @@ def test_rows_that_take_no_part():
 
 
 # B, L, D, K, lens
-CONVS = [(1, 1, 1, 2, None), (2, 5, 8, 4, [5, 0]), (3, 67, 33, 3, [67, 1, 2]), (2, 200, 72, 4, [130, 200]),
+CONVS = [(1, 1, 1, 2, None), (1, 41, 64, 3, None), (2, 33, 48, 2, [30, 33]), (2, 5, 8, 4, [5, 0]), (3, 67, 33, 3, [67, 1, 2]), (2, 200, 72, 4, [130, 200]),
          (1, 129, 1030, 4, None)]
 
 
@@ -369,6 +369,101 @@ def test_conv(case, dtype, silu):
             assert (db is None) == (bias is None)
             if db is not None:
                 assert_within(to_host(db), wb, "f32", "db")
+
+
+def test_runs_of_64_tokens():
+    """A convolution large enough for runs of 64 tokens, bf16, against float64 on the device."""
+    B, L, D, K = 2, 4096, 8192, 4
+    g = torch.Generator(device="cuda").manual_seed(33)
+    x = torch.randn(B, L, D, device="cuda", generator=g).bfloat16()
+    w, b = torch.randn(D, K, device="cuda", generator=g), torch.randn(D, device="cuda", generator=g)
+    lens = [L, 3001]
+    with R.Ssm(D, 8, 1, K, "bf16", B, L, training=False) as f:
+        out = f.conv(x, w, b, lens=ints(lens))
+    for r, n in enumerate(lens):
+        xp = torch.cat([x.new_zeros(K - 1, D), x[r, :n]]).double()
+        p, mag = b.double().expand(n, D).clone(), b.double().abs().expand(n, D).clone()
+        for k in range(K):
+            p += w[:, k].double() * xp[k:k + n]
+            mag += (w[:, k].double() * xp[k:k + n]).abs()
+        want = p * torch.sigmoid(p)
+        # |silu'| <= 1.1; K + 1 fp32 operations on terms of size mag; the gate to 2^-19 and for |p| >= 16 to |p| 2^-23
+        tol = want.abs() * (2.0 ** -8 + 2.0 ** -18 + p.abs() * 2.0 ** -22) + 1.1 * mag * (K + 1) * 2.0 ** -24 + 2.0 ** -120
+        assert ((out[r, :n].double() - want).abs() <= tol).all()
+        assert (out[r, n:] == 0).all()
+
+
+@pytest.mark.parametrize("N", [8, 64])
+def test_many_blocks(N):
+    """Enough channels for every SM without chunks, and a width that no tile divides."""
+    B, L, D = 3, 21, 18001 if N == 8 else 2201
+    s = scan_inputs(B, L, D, N, 1, "f32", 34)
+    want, end = O.ssm_scan(**errs(s))
+    with R.Ssm(D, N, 1, 4, "f32", B, L, training=False) as f:
+        n = 4 * torch.cuda.get_device_properties(0).multi_processor_count
+        assert B * -(-D // (2048 // N)) > n / 3
+        state = f.new_state(B)
+        assert_within(to_host(call_scan(f, dev(s, "f32"), state=state)), want, "f32")
+        assert_within(to_host(state), end, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_rows_alone(dtype):
+    """A batch whose summaries take several chunks a block, against its rows alone, where they take
+    one: the same operations in the same order, so the same bits (sums over the batch aside)."""
+    B, L, D, N = 4, 2048, 1024, 64
+    s = scan_inputs(B, 1, D, N, 1, "f32", 35)
+    g = torch.Generator(device="cuda").manual_seed(36)
+    rn = lambda *sh: torch.randn(*sh, device="cuda", generator=g).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    u, raw, z, do, Bm, Cm = rn(B, L, D), rn(B, L, D), rn(B, L, D), rn(B, L, D), rn(B, L, 1, N), rn(B, L, 1, N)
+    A, skip, bias = (to_dev(s[k], "f32") for k in ("A", "skip", "dt_bias"))
+    with R.Ssm(D, N, 1, 4, dtype, B, L) as f:
+        whole = f.scan_backward(u, raw, A, Bm, Cm, do, skip=skip, z=z, dt_bias=bias)
+        rows = [f.scan_backward(*(t[b:b + 1] for t in (u, raw)), A, *(t[b:b + 1] for t in (Bm, Cm, do)), skip=skip,
+                                z=z[b:b + 1], dt_bias=bias) for b in range(B)]
+    for k in ("du", "ddt", "dz", "dB", "dC"):
+        assert torch.equal(whole[k], torch.cat([r[k] for r in rows])), k
+
+
+def test_offsets_past_32_bits():
+    """A row of more than 2^31 elements against its second half alone, continued from the state; a pool of
+    more than 2^31 states, stepped and copied at its far end."""
+    D, N, L = 2048, 16, 1100000
+    g = torch.Generator(device="cuda").manual_seed(37)
+    rn = lambda *sh: torch.randn(*sh, device="cuda", generator=g, dtype=torch.bfloat16)
+    u, raw, Bm, Cm = rn(1, L, D), rn(1, L, D), rn(1, L, 1, N), rn(1, L, 1, N)
+    A = -torch.arange(1, N + 1, device="cuda").float().expand(D, N).contiguous()
+    w = torch.randn(D, 4, device="cuda", generator=g)
+    half = 1050000
+    assert half * D > 2 ** 31
+    with R.Ssm(D, N, 1, 4, "bf16", 1, L, training=False) as f:
+        state, st2 = f.new_state(1), f.new_state(1)
+        out = f.scan(u, raw, A, Bm, Cm, state=state)
+        part = lambda t, a, b: t[:, a:b].contiguous()
+        f.scan(*(part(t, 0, half) for t in (u, raw)), A, *(part(t, 0, half) for t in (Bm, Cm)), state=st2)
+        tail = f.scan(*(part(t, half, L) for t in (u, raw)), A, *(part(t, half, L) for t in (Bm, Cm)), state=st2)
+        # the two cut their tokens into other chunks: sums in fp32 that differ in their last places, which can
+        # turn a rounding to bf16, so by one step of it, 2^-7 of the value at most
+        assert (out[:, half:].float() - tail.float()).abs().max() <= 2.0 ** -7 * tail.float().abs().max()
+        torch.testing.assert_close(state, st2, rtol=1e-4, atol=1e-5)
+        del out, tail, raw
+        win, w2 = f.new_window(1), f.new_window(1)
+        c = f.conv(u, w, window=win)
+        f.conv(part(u, 0, half), w, window=w2)
+        assert torch.equal(c[:, half:], f.conv(part(u, half, L), w, window=w2)) and torch.equal(win, w2)
+        del c, u, Bm, Cm
+        P = 70000
+        assert (P - 1) * D * N > 2 ** 31
+        pool = torch.empty(P, D, N, device="cuda")
+        pool[P - 1] = state[0]
+        x, dt, B1, C1 = rn(1, D), rn(1, D), rn(1, 1, N), rn(1, 1, N)
+        y = f.scan_step(x, dt, A, B1, C1, pool, pages=ints([P - 1]))
+        assert torch.equal(y, f.scan_step(x, dt, A, B1, C1, state)) and torch.equal(pool[P - 1], state[0])
+        assert R.pages_copy(pool, pool, ints([P - 1]), ints([P - 2])).item() == 1
+        assert torch.equal(pool[P - 2], state[0])
+        R.pages_clear(pool, ints([P - 2]))
+        assert (pool[P - 2] == 0).all() and torch.equal(pool[P - 1], state[0])
+        assert R.pages_compact(pool, ints([P - 1]))[0].item() == 0 and torch.equal(pool[0], state[0])
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
