@@ -241,8 +241,8 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
                 if (MODE != SCAN_SUM) cc = C2[n];
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    h[c][2 * n] = fma2(a[c][2 * n], h[c][2 * n], mul2(x2[c], bb.x));
-                    h[c][2 * n + 1] = fma2(a[c][2 * n + 1], h[c][2 * n + 1], mul2(x2[c], bb.y));
+                    h[c][2 * n] = fma2(x2[c], bb.x, mul2(a[c][2 * n], h[c][2 * n]));
+                    h[c][2 * n + 1] = fma2(x2[c], bb.y, mul2(a[c][2 * n + 1], h[c][2 * n + 1]));
                     if (GRAD) {
                         P[c][2 * n] = mul2(P[c][2 * n], a[c][2 * n]);
                         P[c][2 * n + 1] = mul2(P[c][2 * n + 1], a[c][2 * n + 1]);

@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     const uint64_t d2 = pack2(dd[c], dd[c]), x2 = pack2(xx[c], xx[c]);
-                    h[c][0] = fma2(ex2_2(fma2(A2[c][0], d2, mean2)), h[c][0], mul2(x2, bb.x));
-                    h[c][1] = fma2(ex2_2(fma2(A2[c][1], d2, mean2)), h[c][1], mul2(x2, bb.y));
+                    h[c][0] = fma2(x2, bb.x, mul2(ex2_2(fma2(A2[c][0], d2, mean2)), h[c][0]));
+                    h[c][1] = fma2(x2, bb.y, mul2(ex2_2(fma2(A2[c][1], d2, mean2)), h[c][1]));
                 }
             }
         }
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
                         for (int n = 0; n < 2; ++n) {
                             a[k][n] = ex2_2(fma2(A2[c][n], d2, mean2));
                             hp[k][n] = hc[n];
-                            hc[n] = fma2(a[k][n], hc[n], mul2(x2, n ? bb.y : bb.x));
+                            hc[n] = fma2(x2, n ? bb.y : bb.x, mul2(a[k][n], hc[n]));
                         }
                     }
                 }
