@@ -53,12 +53,17 @@ __device__ __forceinline__ void load_taps(const float* weight, const float* bias
 }
 
 // Grid: channel blocks x runs x rows.  A run of R tokens is walked 8 at a time (4 in
-// fp32), the two steps after it in flight.  [4, 8192, 1024] bf16: 34 us (4.0 TB/s; 43
+// fp32), the two steps after it in flight.  [4, 8192, 1024] bf16: 31 us (4.3 TB/s; 43
 // with the next rows in registers, 55 with 8 tokens a thread and no overlap).
 constexpr int kConvStages = 3;
 
+// Blocks an SM: their registers and rings allow for them.
+constexpr int kConvPerSm = 6;
+template <typename T>
+__host__ __device__ constexpr int conv_bwd_per_sm() { return sizeof(T) == 2 ? 4 : 3; }
+
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kConvThreads) k_conv(ConvArgs a, int D, int cblocks, int runs, int R) {
+__global__ void __launch_bounds__(kConvThreads, kConvPerSm) k_conv(ConvArgs a, int D, int cblocks, int runs, int R) {
     constexpr int U = sizeof(T) == 4 ? 4 : 8;
     const int cb = blockIdx.x % cblocks, rest = blockIdx.x / cblocks;
     const int run = rest % runs, b = rest / runs;
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvArgs a, int D, i
 // The run's sums of dw and dbias go to a row of the workspace, added in a fixed order
 // by k_conv_reduce.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, conv_bwd_per_sm<T>())
 k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
     const int cb = blockIdx.x % cblocks, rest = blockIdx.x / cblocks;
     const int run = rest % runs, b = rest / runs;
@@ -346,15 +351,25 @@ static void conv_dispatch(const SsmHandle& h, bool vec, A... args) {
 
 static int conv_cblocks(int D, int V) { return (D + kConvThreads * V - 1) / (kConvThreads * V); }
 
+// Tokens a run so that the blocks come to whole waves of per_sm on every SM, with about
+// 128 tokens at most and `least` at least ([4, 8192, 1024] bf16 in runs of 72, one wave:
+// 30.7 us; of 32, 2.2 waves: 33.9).
+static int run_tokens(const SsmHandle& h, int cb, int B, int L, int per_sm, int U, int least) {
+    const long long slots = (long long)h.num_sms * per_sm, columns = (long long)cb * B;
+    const long long waves = (columns * L + slots * 256 - 1) / (slots * 256);
+    long long runs = slots * waves / columns;
+    if (runs < 1) runs = 1;
+    long long R = (L + runs - 1) / runs;
+    if (R < least) R = least;
+    return (int)((R + U - 1) / U * U);
+}
+
 template <typename T, int V, int K>
 struct ConvPrompt {
     static void go(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
         constexpr int VP = V < 4 ? V : 4;
         const int cb = conv_cblocks(h.D, VP);
-        // Runs of 64 tokens where they fill the SMs with 8 blocks each, down to 8 where they do not
-        int R = 64;
-        while (R > 8 && (long long)cb * a.B * ((a.L + R - 1) / R) < (long long)h.num_sms * 8) R /= 2;
-        const int runs = (a.L + R - 1) / R;
+        const int R = run_tokens(h, cb, a.B, a.L, kConvPerSm, 8, 8), runs = (a.L + R - 1) / R;
         k_conv<T, VP, K><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs, R);
     }
 };
@@ -367,23 +382,28 @@ struct ConvStep {
     }
 };
 
-// Tokens of a backward run: long enough that the K-1 tokens formed twice and the
-// run's row of partial sums stay small next to it.
-constexpr int kConvBwdRun = 64;
+// Tokens of a backward run at least: the K-1 tokens formed twice and the run's row
+// of partial sums stay small next to it.
+constexpr int kConvBwdRun = 16;
 
 template <typename T, int V, int K>
 struct ConvBwd {
     static void go(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {
         constexpr int VB = V < 4 ? V : 4;   // the sums of 8 channels would take 144 registers
-        const int cb = conv_cblocks(h.D, VB), runs = (a.L + kConvBwdRun - 1) / kConvBwdRun;
-        k_conv_bwd<T, VB, K><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs, kConvBwdRun, h.ws);
+        const int cb = conv_cblocks(h.D, VB);
+        const int R = run_tokens(h, cb, a.B, a.L, conv_bwd_per_sm<T>(), 4, kConvBwdRun), runs = (a.L + R - 1) / R;
+        k_conv_bwd<T, VB, K><<<(unsigned)cb * runs * a.B, kConvThreads, 0, st>>>(a, h.D, cb, runs, R, h.ws);
         const int n = h.D * (K + 1);
         k_conv_reduce<<<(n + 31) / 32, 256, 0, st>>>(h.ws, a.B * runs, h.D, K, a.dweight, a.dbias);
     }
 };
 
+// A row of partial sums a run.  run_tokens gives B rows (one run each) or slots * waves / cblocks at most,
+// and waves <= cblocks B L / (128 slots) + 1: together less than B + B L / 128 + slots.
 size_t conv_backward_ws(const SsmHandle& h) {
-    return (size_t)h.max_B * ((h.max_L + kConvBwdRun - 1) / kConvBwdRun) * h.D * (h.K + 1);
+    const size_t slots = (size_t)h.num_sms * conv_bwd_per_sm<__nv_bfloat16>();   // the larger of the two
+    const size_t rows = (size_t)h.max_B * (1 + (h.max_L + 127) / 128) + slots;
+    return rows * h.D * (h.K + 1);
 }
 
 favor_status conv_prompt(const SsmHandle& h, const ConvArgs& a, cudaStream_t st) {

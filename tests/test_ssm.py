@@ -371,8 +371,8 @@ def test_conv(case, dtype, silu):
                 assert_within(to_host(db), wb, "f32", "db")
 
 
-def test_runs_of_64_tokens():
-    """A convolution large enough for runs of 64 tokens, bf16, against float64 on the device."""
+def test_long_runs():
+    """A convolution large enough for runs of 128 tokens, bf16, against float64 on the device."""
     B, L, D, K = 2, 4096, 8192, 4
     g = torch.Generator(device="cuda").manual_seed(33)
     x = torch.randn(B, L, D, device="cuda", generator=g).bfloat16()
