@@ -429,15 +429,17 @@ __global__ void __launch_bounds__(128) k_scan_chain(ScanArgs p, ScanPlan pl, Sca
     constexpr int K = 8;
     float e[K], s[K], f[K], w[K];   // chunks j0 .., and (backward call) used-1-j0, downwards
     auto fetch = [&](int j0) {
+        // the last one's own end is not asked for, nor what the first hands back
+        const int n = used - 1 - j0;
+        const float *ph = hs + (size_t)j0 * DN, *ps = sdt + (size_t)j0 * D;
+        const float *pm = GRAD ? ms + (size_t)max(n, 0) * DN : nullptr, *pw = sdt + (size_t)max(n, 0) * D;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const bool in = j0 + k < used - 1;   // the last one's own end is not asked for, nor what the first hands back
-            const int j = in ? j0 + k : 0, m = in ? used - 1 - j0 - k : 0;
-            e[k] = in ? hs[(size_t)j * DN] : 0.f;
-            s[k] = in ? sdt[(size_t)j * D] : 0.f;
+            e[k] = k < n ? ph[k * DN] : 0.f;
+            s[k] = k < n ? ps[k * D] : 0.f;
             if (GRAD) {
-                f[k] = in ? ms[(size_t)m * DN] : 0.f;
-                w[k] = in ? sdt[(size_t)m * D] : 0.f;
+                f[k] = k < n ? pm[-k * DN] : 0.f;
+                w[k] = k < n ? pw[-k * D] : 0.f;
             }
         }
     };
@@ -454,13 +456,15 @@ __global__ void __launch_bounds__(128) k_scan_chain(ScanArgs p, ScanPlan pl, Sca
             }
         }
         fetch(j0 + K);
+        float* ph = hs + (size_t)j0 * DN;
+        float* pm = GRAD ? ms + (size_t)(used - 1 - j0) * DN : nullptr;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (j0 + k >= used) break;
-            hs[(size_t)(j0 + k) * DN] = h;
+            ph[k * DN] = h;
             h = fmaf(s0[k], h, e0[k]);
             if (GRAD) {
-                ms[(size_t)(used - 1 - j0 - k) * DN] = mu;
+                pm[-k * DN] = mu;
                 mu = fmaf(w0[k], mu, f0[k]);
             }
         }

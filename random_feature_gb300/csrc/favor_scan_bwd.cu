@@ -18,7 +18,7 @@
 // lanes (halving exchanges: a value costs a shuffle, an add and two selects), the rest
 // staging and the per-element functions; 62% of the issue slots are used with three
 // warps a scheduler, and 68% of the shared-memory pipe.  At [4, 4096, 1024] bf16: 337
-// us, beside 133 for the summaries, 28 for their chain and 23 for the last sums; 620
+// us, beside 129 for the summaries, 24 for their chain and 23 for the last sums; 620
 // us with one channel a thread in plain FMAs, 449 with both channels' states in 255
 // registers and two blocks an SM, 396 before dt was kept for the way back.
 #include <type_traits>
