@@ -141,6 +141,30 @@ def test_scan_edges_of_the_step(dtype):
                 assert_within(to_host(g[k]), w, dtype if k in ("du", "ddt", "dB", "dC", "dz") else "f32", k)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_state_without_decay_stands_still(dtype):
+    """Steps whose softplus underflows to zero, and rates of zero, leave a state as it is to the last bit,
+    through a prompt in chunks and through single tokens."""
+    B, L, D, N = 1, 3000, 48, 16
+    s = scan_inputs(B, L, D, N, 1, dtype, 38)
+    s["skip"] = s["z"] = s["dt_bias"] = None
+    h0 = torch.from_numpy(np.random.default_rng(39).standard_normal((B, D, N)).astype(np.float32)).cuda()
+    with R.Ssm(D, N, 1, 4, dtype, B, L) as f:
+        for still in ("raw", "A"):
+            d = dev(s, dtype)
+            if still == "raw":
+                d["raw"].fill_(-200.0)              # dt = 0: nothing comes in, nothing decays
+            else:
+                d["A"].zero_()                      # nothing decays; nothing comes in either
+                d["u"].zero_()
+            state = h0.clone()
+            call_scan(f, d, state=state)
+            assert torch.equal(state, h0)
+            for t in range(3):
+                call_step(f, d, t, state)
+            assert torch.equal(state, h0)
+
+
 def test_nan_behind_a_row_stays_there():
     """Nothing behind a row's end is read or written."""
     B, L, D, N = 3, 140, 24, 16
