@@ -111,7 +111,11 @@ def _at(t):
 class Ssm:
     """Owns one handle of the convolution and the scan; checks shapes, dtypes and devices before
     calling the C ABI.  Batches are token-major: [B, L, D], B and C [B, L, G, N]; a step call takes
-    the same without L.  ``training=False`` leaves the backward calls' workspace out."""
+    the same without L.  ``training=False`` leaves the backward calls' workspace out.
+
+    ``scan`` and the backward calls use the handle's workspace: of one object, such calls (and
+    replays of graphs that hold them) must not overlap on the device; use an object a stream.
+    ``conv``, the step calls and the page functions use none."""
 
     def __init__(self, D, N, G, K, dtype, max_B, max_L, training=True):
         import torch
