@@ -375,11 +375,11 @@ typedef struct favor_ssm_s* favor_ssm;
 /*
  * favor_ssm_create -- a handle for D channels, N states, G groups, K taps.
  * Supported: N in {8, 16, 32, 64}, K in {2, 3, 4} (else FAVOR_ERR_UNSUPPORTED);
- * D a multiple of G, of any size up to 2^20; max_B*max_L up to 2^30;
- * max_B*D up to 2^30; max_B*max_L*D, max_B*max_L*G*N and max_B*D*N up to 2^36.  training != 0 allocates the backward calls'
- * workspace (8*N*G bytes a token for every 1024 / N channels of a group, and
- * 12*N*D bytes for every 32 tokens of a row); without it they give
- * FAVOR_ERR_UNSUPPORTED.
+ * D a multiple of G, of any size up to 2^20; max_B*max_L and max_B*D up to 2^30;
+ * max_B*max_L*D, max_B*max_L*G*N and max_B*D*N up to 2^36.  training != 0
+ * allocates the backward calls' workspace (8*N*G bytes a token for every 1024 / N
+ * channels of a group, and 12*N*D bytes for every 32 tokens of a row); without it
+ * they give FAVOR_ERR_UNSUPPORTED.
  */
 FAVOR_API favor_status favor_ssm_create(favor_ssm* out, int D, int N, int G, int K, favor_dtype dtype, int max_B,
                                         int max_L, int training);
