@@ -160,6 +160,30 @@ def _stream(stream, like):
     return stream.cuda_stream
 
 
+def _made_on(stream, device, make):
+    """What ``make()`` gives, a tensor or a tuple of tensors and Nones, for a call on ``stream`` to write.
+
+    On a stream other than torch's current one the tensors are allocated, and whatever fills them
+    enqueued, in that stream's order: in the current one's a fill could land behind the call, and a block
+    that was freed a moment ago could still have queued readers and writers.  The current stream is noted
+    with the allocator, so that it may read them, once it waits for the call, up to the moment they are freed."""
+    if stream is None:
+        return make()
+    import torch
+    raw = stream if isinstance(stream, int) else stream.cuda_stream
+    if raw == 1:                # the driver's second name of the legacy default stream
+        raw = 0
+    current = torch.cuda.current_stream(device)
+    if raw == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device)):
+        made = make()
+    for t in made if isinstance(made, tuple) else (made,):
+        if t is not None:
+            t.record_stream(current)
+    return made
+
+
 def favor_create(H, m, d, dv, kind, dtype, omega, data_scale, max_B, max_L) -> int:
     """Create a handle; ``omega`` is a host float32 array [H, m, d] ([H, m/2, d] for the
     hyperbolic and trigonometric kinds).  Returns the handle (int)."""

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 from operator import attrgetter
 
-from .favor import DTYPE_CODES, _check, _ptr, _stream, lib
+from .favor import DTYPE_CODES, _check, _made_on, _ptr, _stream, lib
 
 __all__ = [
     "favor_ssm_create", "favor_ssm_destroy", "favor_conv_causal", "favor_conv_causal_step",
@@ -115,7 +115,10 @@ class Ssm:
 
     ``scan`` and the backward calls use the handle's workspace: of one object, such calls (and
     replays of graphs that hold them) must not overlap on the device; use an object a stream.
-    ``conv``, the step calls and the page functions use none."""
+    ``conv``, the step calls and the page functions use none.
+
+    A call with ``stream`` makes its outputs in that stream's order; that the inputs are ready there, and
+    that whoever reads the outputs on another stream waits for the call, is the caller's to arrange."""
 
     def __init__(self, D, N, G, K, dtype, max_B, max_L, training=True):
         import torch
@@ -156,11 +159,12 @@ class Ssm:
             raise ValueError(f"{name}: expected {dims} dimensions, got {list(x.shape)}")
         return tuple(x.shape[:-1])
 
-    def _out(self, like, out, lens=None):
+    def _out(self, like, out, stream, lens=None):
         """The output: rows behind a row's end are left as they are, so a new one starts at zero."""
         if out is None:
             import torch
-            return torch.empty_like(like) if lens is None else torch.zeros_like(like)
+            new = torch.empty_like if lens is None else torch.zeros_like
+            return new(like) if stream is None else _made_on(stream, self.device, lambda: new(like))
         self._check_all(((out, _kind(like), "out"),))
         return out
 
@@ -190,7 +194,7 @@ class Ssm:
         past and keeps the row's last inputs."""
         B, L = lead = self._lead(x, 3, "x")
         P = self._conv_args(lead, x, weight, bias, window, pages, lens)
-        out = self._out(x, out, lens)
+        out = self._out(x, out, stream, lens)
         _check(self._lib.favor_conv_causal(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
                                            _at(window), _at(pages), P, _at(lens), out.data_ptr(), B, L,
                                            _raw_stream(stream, self._index)), "favor_conv_causal")
@@ -200,7 +204,7 @@ class Ssm:
         """One token a row, x [B, D]; the rows' windows move on."""
         lead = self._lead(x, 2, "x")
         P = self._conv_args(lead, x, weight, bias, window, pages, None)
-        out = self._out(x, out)
+        out = self._out(x, out, stream)
         _check(self._lib.favor_conv_causal_step(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
                                                 _at(window), _at(pages), P, out.data_ptr(), lead[0],
                                                 _raw_stream(stream, self._index)), "favor_conv_causal_step")
@@ -212,9 +216,9 @@ class Ssm:
         B, L = lead = self._lead(x, 3, "x")
         self._conv_args(lead, x, weight, bias, None, None, lens)
         self._check_all(((dout, _kind(x), "dout"),))
-        dx = torch.empty_like(x)
-        dweight = torch.empty_like(weight)
-        dbias = None if bias is None else torch.empty_like(bias)
+        new = torch.empty_like
+        dx, dweight, dbias = _made_on(stream, self.device,
+                                      lambda: (new(x), new(weight), None if bias is None else new(bias)))
         _check(self._lib.favor_conv_causal_backward(self.handle, x.data_ptr(), weight.data_ptr(), _at(bias), int(silu),
                                                     _at(lens), dout.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
                                                     _at(dbias), B, L, _raw_stream(stream, self._index)),
@@ -239,7 +243,7 @@ class Ssm:
         leaves the state behind the row's last token."""
         B, L = lead = self._lead(u, 3, "u")
         P = self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, lens)
-        out = self._out(u, out, lens)
+        out = self._out(u, out, stream, lens)
         _check(self._lib.favor_ssm_scan(self.handle, u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
                                         Cm.data_ptr(), _at(skip), _at(z), _at(dt_bias), _at(state), _at(pages), P,
                                         _at(lens), out.data_ptr(), B, L, _raw_stream(stream, self._index)),
@@ -250,7 +254,7 @@ class Ssm:
         """One token a row: u, dt [B, D], Bm, Cm [B, G, N]; the rows' states move on."""
         lead = self._lead(u, 2, "u")
         P = self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, None)
-        out = self._out(u, out)
+        out = self._out(u, out, stream)
         _check(self._lib.favor_ssm_scan_step(self.handle, u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
                                              Cm.data_ptr(), _at(skip), _at(z), _at(dt_bias), _at(state), _at(pages),
                                              P, out.data_ptr(), lead[0], _raw_stream(stream, self._index)),
@@ -265,9 +269,9 @@ class Ssm:
         self._scan_args(lead, u, dt, A, Bm, Cm, skip, z, dt_bias, None, None, lens)
         self._check_all(((dout, _kind(u), "dout"),))
         new = torch.empty_like
-        gr = dict(du=new(u), ddt=new(dt), dA=torch.empty_like(A), dB=new(Bm), dC=new(Cm),
-                  dskip=None if skip is None else torch.empty_like(skip), dz=None if z is None else new(z),
-                  ddt_bias=None if dt_bias is None else torch.empty_like(dt_bias))
+        gr = dict(zip(("du", "ddt", "dA", "dB", "dC", "dskip", "dz", "ddt_bias"), _made_on(
+            stream, self.device,
+            lambda: tuple(None if t is None else new(t) for t in (u, dt, A, Bm, Cm, skip, z, dt_bias)))))
         _check(self._lib.favor_ssm_scan_backward(self.handle, u.data_ptr(), dt.data_ptr(), A.data_ptr(),
                                                  Bm.data_ptr(), Cm.data_ptr(), _at(skip), _at(z), _at(dt_bias),
                                                  _at(lens), dout.data_ptr(), *(_at(g) for g in gr.values()), B, L,
@@ -329,7 +333,7 @@ def pages_copy(dst_pool, src_pool, src, dst, stream=None):
     n = src.shape[0]
     if n != dst.shape[0]:
         raise ValueError(f"src names {n} pages and dst {dst.shape[0]}")
-    done = torch.empty_like(src)
+    done = _made_on(stream, src.device, lambda: torch.empty_like(src))
     _check(_on(index, lambda: lib().favor_pages_copy(dst_pool.data_ptr(), dst_pool.shape[0], src_pool.data_ptr(),
                                                      src_pool.shape[0], pb, src.data_ptr(), dst.data_ptr(), n,
                                                      done.data_ptr(), _raw_stream(stream, index))),
@@ -358,9 +362,8 @@ def pages_compact(pool, table, others=(), stream=None):
         sizes.append(_page_bytes(o, f"others[{i}]"))
         if o.shape[0] != P or o.get_device() != index:
             raise ValueError(f"others[{i}]: expected {P} pages on cuda:{index}")
-    new_table = torch.empty_like(table)
-    n_live = table.new_empty(1)
-    page_map = table.new_empty(P) if sizes else None
+    new_table, n_live, page_map = _made_on(stream, table.device, lambda: (
+        torch.empty_like(table), table.new_empty(1), table.new_empty(P) if sizes else None))
 
     def call():
         s = _raw_stream(stream, index)
