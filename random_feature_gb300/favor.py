@@ -332,17 +332,18 @@ class Favor:
             raise ValueError(f"{name}: expected contiguous CUDA {self._tdtype()} [{B},{self.H},{L},{w}], "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
-    def _new(self, like, B, L, w, out):
+    def _new(self, like, B, L, w, out, stream):
         import torch
         if out is None:
-            out = torch.empty((B, self.H, L, w), dtype=self._tdtype(), device=like.device)
+            return _made_on(stream, like.device, lambda: torch.empty((B, self.H, L, w), dtype=self._tdtype(),
+                                                                     device=like.device))
         self._chk(out, B, L, w, "out")
         return out
 
     def feature_map(self, x, out=None, stream=None):
         B, _, L, _ = x.shape
         self._chk(x, B, L, self.d, "x")
-        out = self._new(x, B, L, self.m, out)
+        out = self._new(x, B, L, self.m, out, stream)
         favor_feature_map(self.handle, x, out, B, L, stream)
         return out
 
@@ -351,7 +352,7 @@ class Favor:
         self._chk(q, B, L, self.d, "q")
         self._chk(k, B, L, self.d, "k")
         self._chk(v, B, L, self.dv, "v")
-        out = self._new(q, B, L, self.dv, out)
+        out = self._new(q, B, L, self.dv, out, stream)
         (favor_attn_causal if causal else favor_attn_bidir)(self.handle, q, k, v, out, B, L, stream)
         return out
 
@@ -362,8 +363,7 @@ class Favor:
         for t, w, name in ((q, self.d, "q"), (k, self.d, "k"), (v, self.dv, "v"), (dout, self.dv, "dout")):
             self._chk(t, B, L, w, name)
         if grads is None:
-            grads = (self._new(q, B, L, self.d, None), self._new(q, B, L, self.d, None),
-                     self._new(q, B, L, self.dv, None))
+            grads = tuple(self._new(q, B, L, w, None, stream) for w in (self.d, self.d, self.dv))
         dq, dk, dv = grads
         self._chk(dq, B, L, self.d, "dq")
         self._chk(dk, B, L, self.d, "dk")
@@ -382,7 +382,7 @@ class Favor:
         if tuple(gate.shape) != (B, self.H, L) or gate.dtype != torch.float32 or not gate.is_cuda \
                 or not gate.is_contiguous():
             raise ValueError(f"gate: expected contiguous CUDA float32 [{B},{self.H},{L}]")
-        out = self._new(q, B, L, self.dv, out)
+        out = self._new(q, B, L, self.dv, out, stream)
         favor_attn_causal_gated(self.handle, q, k, v, gate, out, B, L, stream)
         return out
 
@@ -396,7 +396,7 @@ class Favor:
         if tuple(gate.shape) != (B, self.H, T) or gate.dtype != torch.float32 or not gate.is_cuda \
                 or not gate.is_contiguous():
             raise ValueError(f"gate: expected contiguous CUDA float32 [{B},{self.H},{T}]")
-        out = self._new(q, B, T, self.dv, out)
+        out = self._new(q, B, T, self.dv, out, stream)
         favor_attn_causal_step_gated(self.handle, q, k, v, gate, out, state, B, T, stream)
         return out
 
@@ -421,7 +421,7 @@ class Favor:
         self._chk(k, B, L, self.d, "k")
         self._chk(v, B, L, self.dv, "v")
         if state is None:
-            state = self.new_state(B)
+            state = _made_on(stream, k.device, lambda: self.new_state(B))
         self._chk_state(state, B)
         favor_kv_state(self.handle, k, v, state, B, L, stream)
         return state
@@ -430,7 +430,7 @@ class Favor:
         B, _, L, _ = q.shape
         self._chk(q, B, L, self.d, "q")
         self._chk_state(state, B)
-        out = self._new(q, B, L, self.dv, out)
+        out = self._new(q, B, L, self.dv, out, stream)
         favor_attn_from_state(self.handle, q, state, out, B, L, stream)
         return out
 
@@ -441,7 +441,7 @@ class Favor:
         self._chk(k, B, T, self.d, "k")
         self._chk(v, B, T, self.dv, "v")
         self._chk_state(state, B)
-        out = self._new(q, B, T, self.dv, out)
+        out = self._new(q, B, T, self.dv, out, stream)
         favor_attn_causal_step(self.handle, q, k, v, out, state, B, T, stream)
         return out
 

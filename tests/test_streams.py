@@ -147,6 +147,36 @@ def test_page_tables_belong_to_the_given_stream(log, monkeypatch, given):
     assert all(s == CUR for _, s in log.noted) and len(log.noted) >= (3 if given else 0)
 
 
+FAVOR = {
+    "feature_map": lambda f, t, s: f.feature_map(t, stream=s),
+    "attn": lambda f, t, s: f.attn(t, t, t, stream=s),
+    "attn_causal": lambda f, t, s: f.attn(t, t, t, causal=True, stream=s),
+    "attn_backward": lambda f, t, s: f.attn_backward(t, t, t, t, stream=s),
+    "attn_causal_gated": lambda f, t, s: f.attn_causal_gated(t, t, t, t.gate, stream=s),
+    "causal_step_gated": lambda f, t, s: f.causal_step_gated(t, t, t, t.gate, t, stream=s),
+    "kv_state": lambda f, t, s: f.kv_state(t, t, stream=s),
+    "attn_from_state": lambda f, t, s: f.attn_from_state(t, t, stream=s),
+    "causal_step": lambda f, t, s: f.causal_step(t, t, t, t, stream=s),
+}
+
+
+@pytest.mark.parametrize("given", [SIDE, None])
+@pytest.mark.parametrize("call", FAVOR)
+def test_favor_outputs_belong_to_the_given_stream(log, call, given):
+    f = object.__new__(R.Favor)
+    f.H, f.m, f.d, f.dv, f.dtype, f.handle = 2, 8, 4, 4, "f32", None
+    f._chk = f._chk_state = lambda *a: None
+    yes = lambda: True
+    gate = types.SimpleNamespace(shape=(1, 2, 3), dtype=torch.float32, is_cuda=True, is_contiguous=yes,
+                                 data_ptr=lambda: 64)
+    t = types.SimpleNamespace(shape=(1, 2, 3, 4), device=None, data_ptr=lambda: 64, gate=gate)
+    FAVOR[call](f, t, given)
+    want = SIDE if given else CUR
+    assert log.made and all(m.at == want for m in log.made)
+    assert log.noted == [(m, CUR) for m in log.made if given]
+    assert len(log.calls) == 1 and log.calls[0][1][-1] == want
+
+
 # ---- on the GPU
 def _busy(seconds=0.15):
     """Ordinary work of about that time on the current stream, without waiting for it."""
@@ -209,6 +239,31 @@ def test_ssm_calls_beside_a_busy_stream(call, as_address):
         got = run(side.cuda_stream if as_address else side)
         side.synchronize()
         assert not torch.cuda.current_stream().query()      # the work there was still going on
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["kv_state", "attn_causal", "attn_backward"])
+def test_favor_calls_beside_a_busy_stream(call):
+    import numpy as np
+    B, H, L, d, m = 2, 2, 130, 16, 32
+    omega = np.random.default_rng(2).standard_normal((H, m, d)).astype(np.float32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v, do = (0.5 * torch.randn(B, H, L, d, device="cuda", generator=g) for _ in range(4))
+    with R.Favor(H, m, d, d, "softmax_pos", "f32", omega, 0.5, B, L) as f:
+        run = {"kv_state": lambda s: (f.kv_state(k, v, stream=s),),
+               "attn_causal": lambda s: (f.attn(q, k, v, causal=True, stream=s),),
+               "attn_backward": lambda s: f.attn_backward(q, k, v, do, stream=s)}[call]
+        want = [t.clone() for t in run(None)]
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        _busy()
+        _later_writes([(t.shape, t.dtype) for t in want])
+        got = run(side)
+        side.synchronize()
+        assert not torch.cuda.current_stream().query()
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
