@@ -25,8 +25,10 @@
  * A handle owns device copies of omega, per-head constants and a workspace
  * sized at creation for max_B and max_L.  Calls on one handle must not overlap
  * in time on the device (they share the workspace); use one handle per
- * concurrent stream.  A handle belongs to the device that was current at
- * favor_create; call it with that device current.
+ * concurrent stream.  Nor may two host threads call one favor_handle at once,
+ * on one stream either: a call is several launches, which would mix.  A handle
+ * belongs to the device that was current at favor_create; call it with that
+ * device current.
  */
 #ifndef FAVOR_H
 #define FAVOR_H
@@ -368,6 +370,8 @@ FAVOR_API favor_status favor_destroy(favor_handle h);
  * handle's workspace, so those calls on one handle (a graph's replays among
  * them) must not overlap in time on the device; favor_conv_causal and the step
  * calls use none and may overlap anything that does not share their tensors.
+ * Several host threads may call one handle on one stream: a call's launches are
+ * enqueued together.
  * Outputs and pools must not overlap any other argument (INVALID_ARG).
  */
 typedef struct favor_ssm_s* favor_ssm;

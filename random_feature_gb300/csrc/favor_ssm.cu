@@ -2,6 +2,7 @@
 // checks, handle lifetime, workspace.  Every check runs before anything is
 // enqueued; a failing call launches nothing.
 #include <initializer_list>
+#include <mutex>
 #include <new>
 
 #include "ssm_internal.h"
@@ -200,6 +201,7 @@ favor_status favor_conv_causal_backward(favor_ssm hd, const void* x, const float
     ConvArgs a = {};
     a.x = x; a.weight = weight; a.bias = bias; a.lens = lens; a.dout = dout; a.dx = dx; a.dweight = dweight;
     a.dbias = dbias; a.B = B; a.L = L; a.silu = silu != 0;
+    std::lock_guard<std::mutex> lk(h.enqueue);
     return conv_backward(h, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -223,7 +225,9 @@ static favor_status scan_call(const char* fn, favor_ssm hd, const ScanArgs& a, b
                         {a.lens, (size_t)a.B * 4}};
     if (any_overlap(outs, 2, ins, 10))
         return set_error(FAVOR_ERR_INVALID_ARG, "%s: out and state must not overlap another argument", fn);
-    return (step ? scan_step : scan_prompt)(h, a, reinterpret_cast<cudaStream_t>(stream));
+    if (step) return scan_step(h, a, reinterpret_cast<cudaStream_t>(stream));
+    std::lock_guard<std::mutex> lk(h.enqueue);
+    return scan_prompt(h, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 favor_status favor_ssm_scan(favor_ssm h, const void* u, const void* dt, const float* A, const void* Bm, const void* Cm,
@@ -270,6 +274,7 @@ favor_status favor_ssm_scan_backward(favor_ssm hd, const void* u, const void* dt
     a.u = u; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.skip = skip; a.z = z; a.dt_bias = dt_bias; a.lens = lens;
     a.dout = dout; a.du = du; a.ddt = ddt; a.dA = dA; a.dB = dB; a.dC = dC; a.dskip = dskip; a.dz = dz;
     a.ddt_bias = ddt_bias; a.B = B; a.L = L;
+    std::lock_guard<std::mutex> lk(h.enqueue);
     return scan_backward(h, a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "favor_internal.h"
 
@@ -20,6 +21,9 @@ struct SsmHandle {
     int device, num_sms;
     float* ws;              // one area, laid out per call by the launchers below
     size_t ws_floats;
+    // Held while a call that uses ws is enqueued: it is several launches, and another host thread's,
+    // on the same stream, must not come between them.
+    mutable std::mutex enqueue;
 };
 
 // Rows b of a call and where their state lives.

@@ -115,6 +115,7 @@ class Ssm:
 
     ``scan`` and the backward calls use the handle's workspace: of one object, such calls (and
     replays of graphs that hold them) must not overlap on the device; use an object a stream.
+    Several host threads may call one object on one stream.
     ``conv``, the step calls and the page functions use none.
 
     A call with ``stream`` makes its outputs in that stream's order; that the inputs are ready there, and
