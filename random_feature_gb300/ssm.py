@@ -147,11 +147,13 @@ class Ssm:
                 raise ValueError(f"{name}: expected contiguous {want[1]} {list(want[0])} on {want[2]}, "
                                  f"got {t.dtype} {list(t.shape)} on {t.device}")
 
-    def _pool(self, pool, page, dtype):
+    def _pool(self, pool, page, dtype, name):
         """(number of pages, what the pool has to be)."""
         if pool is None:
             return 0, None
         P = pool.shape[0] if pool.dim() else 0
+        if P == 0:      # its address is NULL, which means that there is none
+            raise ValueError(f"{name}: expected at least one page {list(page)}, got {list(pool.shape)}")
         return P, ((P, *page), dtype, self.device)
 
     @staticmethod
@@ -183,7 +185,7 @@ class Ssm:
     # ---- convolution
     def _conv_args(self, lead, x, weight, bias, window, pages, lens):
         """Checks; the number of window pages."""
-        P, pool = self._pool(window, (self.K - 1, self.D), self._t)
+        P, pool = self._pool(window, (self.K - 1, self.D), self._t, "window")
         rows = (lead[:1], self._i32, self.device)
         self._check_all(((x, (lead + self._dims, self._t, self.device), "x"), (weight, self._weight, "weight"),
                          (bias, self._vec, "bias"), (window, pool, "window"), (pages, rows, "pages"),
@@ -230,7 +232,7 @@ class Ssm:
     def _scan_args(self, lead, u, dt, A, Bm, Cm, skip, z, dt_bias, state, pages, lens):
         """Checks; the number of state pages."""
         dev = self.device
-        P, pool = self._pool(state, (self.D, self.N), self._f32)
+        P, pool = self._pool(state, (self.D, self.N), self._f32, "state")
         seq, mat = (lead + self._dims, self._t, dev), (lead + (self.G, self.N), self._t, dev)
         rows = (lead[:1], self._i32, dev)
         self._check_all(((u, seq, "u"), (dt, seq, "dt"), (z, seq, "z"), (Bm, mat, "Bm"), (Cm, mat, "Cm"),

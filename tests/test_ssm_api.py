@@ -132,3 +132,41 @@ def test_calls_refuse():
                 call()
             assert e.value.status == BAD and "aligned" in str(e.value)
         assert R.favor_launch_count() == n0
+
+
+def _offline_ssm(monkeypatch, calls):
+    """An Ssm of CPU tensors whose library only records the calls."""
+    import torch
+    from random_feature_gb300 import ssm
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, a)) or 0
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    monkeypatch.setattr(ssm, "lib", Lib)
+    f, cpu, f4 = object.__new__(R.Ssm), torch.device("cpu"), torch.float32
+    f.D, f.N, f.G, f.K, f.handle, f.device, f._index, f._lib = 4, 8, 1, 2, None, cpu, 0, Lib()
+    f._t, f._f32, f._i32, f._dims = f4, f4, torch.int32, (4,)
+    f._weight, f._vec, f._A = ((4, 2), f4, cpu), ((4,), f4, cpu), ((4, 8), f4, cpu)
+    return f
+
+
+def test_pools_without_pages_are_refused(monkeypatch):
+    """A pool of no pages has no address: it is refused, not taken for an absent one."""
+    import torch
+    calls = []
+    f = _offline_ssm(monkeypatch, calls)
+    x, bc, A, w = torch.zeros(2, 3, 4), torch.zeros(2, 3, 1, 8), torch.zeros(4, 8), torch.zeros(4, 2)
+    x1, b1 = x[:, 0].contiguous(), bc[:, 0].contiguous()
+    pages = torch.zeros(2, dtype=torch.int32)
+    for kw in ({}, {"pages": pages}):
+        for bad, name in ((lambda: f.conv(x, w, window=torch.zeros(0, 1, 4), **kw), "window"),
+                          (lambda: f.conv_step(x1, w, torch.zeros(0, 1, 4), **kw), "window"),
+                          (lambda: f.scan(x, x, A, bc, bc, state=torch.zeros(0, 4, 8), **kw), "state"),
+                          (lambda: f.scan_step(x1, x1, A, b1, b1, torch.zeros(0, 4, 8), **kw), "state")):
+            with pytest.raises(ValueError, match=name):
+                bad()
+    assert not calls
+    f.conv(x, w, window=torch.zeros(2, 1, 4))
+    f.scan(x, x, A, bc, bc, state=torch.zeros(2, 4, 8))
+    assert [c[0] for c in calls] == ["favor_conv_causal", "favor_ssm_scan"]
