@@ -360,6 +360,7 @@ def pages_compact(pool, table, others=(), stream=None):
     import torch
     pb, index, P = _page_bytes(pool, "pool"), pool.get_device(), pool.shape[0]
     _indices(table, index, "table")
+    others = tuple(others)      # walked twice
     sizes = []
     for i, o in enumerate(others):
         sizes.append(_page_bytes(o, f"others[{i}]"))

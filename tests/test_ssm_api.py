@@ -170,3 +170,40 @@ def test_pools_without_pages_are_refused(monkeypatch):
     f.conv(x, w, window=torch.zeros(2, 1, 4))
     f.scan(x, x, A, bc, bc, state=torch.zeros(2, 4, 8))
     assert [c[0] for c in calls] == ["favor_conv_causal", "favor_ssm_scan"]
+
+
+def test_compaction_moves_pools_of_a_generator(monkeypatch):
+    """The other pools may come from any iterable, one that can be walked once among them."""
+    import torch
+    from types import SimpleNamespace
+    from random_feature_gb300 import ssm
+    calls = []
+    f = _offline_ssm(monkeypatch, calls)
+    monkeypatch.setattr(ssm, "lib", lambda: f._lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    pool = lambda at: SimpleNamespace(numel=lambda: 8, dim=lambda: 2, is_cuda=True, is_contiguous=lambda: True,
+                                      shape=(4, 2), element_size=lambda: 4, get_device=lambda: 0, data_ptr=lambda: at)
+    table = torch.tensor([3, 1], dtype=torch.int32)
+    monkeypatch.setattr(ssm, "_indices", lambda *a: None)
+    R.pages_compact(pool(64), table, others=(pool(at) for at in (128, 256)))
+    assert [c[0] for c in calls] == ["favor_pages_compact", "favor_pages_move", "favor_pages_move"]
+    assert [c[1][0] for c in calls] == [64, 128, 256]
+    calls.clear()
+    bad = pool(256)
+    bad.shape = (5, 2)
+    with pytest.raises(ValueError, match=r"others\[1\]"):      # before anything is moved
+        R.pages_compact(pool(64), table, others=(p for p in (pool(128), bad)))
+    assert not calls
+
+
+@pytest.mark.gpu
+def test_compaction_of_a_generator_on_the_device():
+    import torch
+    pool = torch.arange(6, device="cuda", dtype=torch.float32).view(6, 1)
+    wins = [pool * 10, pool * 100]
+    table = torch.tensor([5, 2, 4], dtype=torch.int32, device="cuda")
+    new, live = R.pages_compact(pool, table, others=(w for w in wins))
+    assert new.tolist() == [1, 2, 0] and live.tolist() == [3]
+    assert pool[:3, 0].tolist() == [4, 5, 2]
+    for w, scale in zip(wins, (10, 100)):
+        assert w[:3, 0].tolist() == [4 * scale, 5 * scale, 2 * scale]
