@@ -116,7 +116,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+// log2 e in two parts (Cody and Waite's split): the nearest float and what it leaves.
+constexpr double kLog2eExact = 1.4426950408889634074;
+constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - (double)kLog2e);
 
 // One pack (4, 8 or 16 bytes) global -> shared, asynchronously; zeros where !ok (src is not read then).
 template <typename P>
@@ -193,16 +195,16 @@ __device__ __forceinline__ float softplus_f(float x) {
 
 // 1 / (1 + e^-x).  For 16-bit storage the approximate forms (relative error
 // below 2^-19 for |x| < 16) are far under the output's rounding of 2^-9.  fp32
-// storage adds what the product with log2 e lost to the exponent and one Newton step
-// to the reciprocal (e is kept finite for it; a NaN comes back through x itself
-// in every product this is used in).
+// storage multiplies e by 1 + r ln 2, r what the rounded product with log2 e lacks
+// of the exact one, taken from the two parts by fused multiply-adds; and takes one
+// Newton step, s + s (1 - d s), on the reciprocal (e is kept finite for it; a NaN
+// comes back through x itself in every product this is used in).
 template <typename T>
 __device__ __forceinline__ float sigmoid_f(float x) {
     const float t = -x * kLog2e;
     float e = ex2_approx(t);
     if (sizeof(T) == 2) return rcp_approx(1.f + e);
-    constexpr float lo = 1.925963033500e-8f;   // log2 e - kLog2e
-    const float r = fmaf(-x, lo, fmaf(-x, kLog2e, -t));
+    const float r = fmaf(-x, kLog2eRest, fmaf(-x, kLog2e, -t));
     if (fabsf(x) < 100.f) e = fmaf(e, r * 0.6931471805599453f, e);   // not of infinities
     e = fminf(e, 1e38f);
     const float d = 1.f + e, s = rcp_approx(d);

@@ -590,3 +590,17 @@ def test_block_as_used():
         assert_within(to_host(gr[k]), v, "f32", k)
     for a, b in zip((dx, dw, db), O.conv_causal_backward(Err(x), Err(w), wg["du"], Err(bias))):
         assert_within(to_host(a), b, "f32")
+
+
+def test_gate_over_its_range():
+    """x sigmoid(x) of fp32 storage, relative to its value, from where it vanishes to where it is x.
+    With U = 2^-24: the exponential's 4 U and 1 U for the factor that mends its argument, 1 U each for
+    1 + e, its reciprocal and the product, so 8 U; below 2^-126 the reciprocal may be flushed to zero."""
+    x = np.concatenate([np.linspace(-90, 90, 40000), np.random.default_rng(40).uniform(-3, 3, 25536)])
+    x = x.astype(np.float32).astype(np.float64).reshape(1, 64, 1024)
+    with R.Ssm(1024, 8, 1, 2, "f32", 1, 64, training=False) as f:
+        w = torch.tensor([0.0, 1.0], device="cuda").expand(1024, 2).contiguous()    # p = x
+        got = to_host(f.conv(to_dev(x, "f32"), w))
+    want = x / (1 + np.exp(-x))
+    tol = 2.0 ** -21 * np.abs(want) + np.abs(x) * 2.0 ** -126
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
