@@ -339,7 +339,7 @@ k_scan(ScanArgs p, ScanPlan pl, ScanWs ws, int D, int G) {
 #pragma unroll
             for (int e = 0; e < V; ++e) d[e] = to_f(rd.v[e]) + bias.v[e];
 #pragma unroll
-            for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
+            for (int e = 0; e < V; e += 2) softplus_2<T>(d[e], d[e + 1]);
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 sm.sdt[ev_t[v]][e * CV + ev_c[v]] = make_float2(d[e], d[e] * to_f(ru.v[e]));
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_step(ScanArgs p, int D, i
         if (mine) from_f(((T*)p.out)[at], 0.f);
         return;
     }
-    const float d = softplus_f(raw), x = d * uu, dl = d * kLog2e;
+    const float d = softplus_f<T>(raw), x = d * uu, dl = d * kLog2e;
     float y[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {

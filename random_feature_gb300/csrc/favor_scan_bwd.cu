@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
                             : to_f(rd.v[e]) + sm.sbias[S::place(cv * V + e)];
             if (!back) {
 #pragma unroll
-                for (int e = 0; e < V; e += 2) softplus_2(d[e], d[e + 1]);
+                for (int e = 0; e < V; e += 2) softplus_2<T>(d[e], d[e + 1]);
             }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) k_bwd_main(ScanArgs p, BwdPlan
                 const float d = sm.d[t - t0 + tt][S::turned(tt, at)], uu = to_f(ru.v[e]), oo = to_f(ro.v[e]);
                 const float2 yl = reinterpret_cast<const float2*>(&sm.dx[tt][pr])[hf];
                 const float y = yl.x, lb = yl.y;
-                const float aq = reinterpret_cast<const float*>(&sm.g[tt][pr])[hf] * 0.6931471805599453f;   // A was scaled by log2 e
+                const float aq = reinterpret_cast<const float*>(&sm.g[tt][pr])[hf] * kLn2;   // A was scaled by log2 e
                 float gg = oo;
                 if (p.z) {
                     const float zz = to_f(rz.v[e]), sg = sigmoid_f<T>(zz);

@@ -116,9 +116,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// log2 e in two parts (Cody and Waite's split): the nearest float and what it leaves.
+// log2 e and ln 2 in two parts (Cody and Waite's split): the nearest float and what it leaves.
 constexpr double kLog2eExact = 1.4426950408889634074;
 constexpr float kLog2e = (float)kLog2eExact, kLog2eRest = (float)(kLog2eExact - (double)kLog2e);
+constexpr double kLn2Exact = 0.69314718055994530942;
+constexpr float kLn2 = (float)kLn2Exact, kLn2Rest = (float)(kLn2Exact - (double)kLn2);
 
 // One pack (4, 8 or 16 bytes) global -> shared, asynchronously; zeros where !ok (src is not read then).
 template <typename P>
@@ -174,9 +176,22 @@ __device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
 
 // ln(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| <= 1, with
 // log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3: the odd series up to s^13 leaves
-// s^14 / 15 < 1.4e-8 of the sum.  Two values at a time for the packed FMA.
+// s^14 / 15 < 1.4e-8 of the sum.  Two values at a time for the packed FMA.  The
+// product of |x| and log2 e is off by half a step, |x| 2^-24 of e and so of the result
+// (3e-6 at -50): of no weight beside a raw step of 16 bits, which leaves |x| 2^-9.  fp32
+// storage multiplies e = 2^t by 1 + d, d = -|x| - t ln 2 with ln 2 in two parts (Cody and
+// Waite's reduction): [8, 4096, 1536] with 16 states 463 us, 457 without.
+template <typename T>
 __device__ __forceinline__ void softplus_2(float& x0, float& x1) {
-    const float e0 = ex2_approx(-fabsf(x0) * kLog2e), e1 = ex2_approx(-fabsf(x1) * kLog2e);
+    const float t0 = -fabsf(x0) * kLog2e, t1 = -fabsf(x1) * kLog2e;
+    float e0 = ex2_approx(t0), e1 = ex2_approx(t1);
+    if constexpr (sizeof(T) == 4) {
+        float d0, d1;
+        const uint64_t t = pack2(-t0, -t1), e = pack2(e0, e1);
+        unpack2(fma2(t, pack2(kLn2Rest, kLn2Rest), fma2(t, pack2(kLn2, kLn2), pack2(-fabsf(x0), -fabsf(x1)))), d0, d1);
+        // infinite t leave no d, and e = 0 (the minimum with a NaN is the other operand; e keeps a NaN of x)
+        unpack2(fma2(e, pack2(fminf(d0, 1.f), fminf(d1, 1.f)), e), e0, e1);
+    }
     const uint64_t s = mul2(pack2(e0, e1), pack2(rcp_approx(2.f + e0), rcp_approx(2.f + e1)));
     const uint64_t q = mul2(s, s);
     uint64_t r = fma2(q, pack2(1.f / 13.f, 1.f / 13.f), pack2(1.f / 11.f, 1.f / 11.f));
@@ -187,9 +202,10 @@ __device__ __forceinline__ void softplus_2(float& x0, float& x1) {
     r = fma2(r, q, pack2(1.f, 1.f));
     unpack2(fma2(mul2(s, pack2(2.f, 2.f)), r, pack2(fmaxf(x0, 0.f), fmaxf(x1, 0.f))), x0, x1);
 }
+template <typename T>
 __device__ __forceinline__ float softplus_f(float x) {
     float y = x;
-    softplus_2(x, y);
+    softplus_2<T>(x, y);
     return x;
 }
 
@@ -205,7 +221,7 @@ __device__ __forceinline__ float sigmoid_f(float x) {
     float e = ex2_approx(t);
     if (sizeof(T) == 2) return rcp_approx(1.f + e);
     const float r = fmaf(-x, kLog2eRest, fmaf(-x, kLog2e, -t));
-    if (fabsf(x) < 100.f) e = fmaf(e, r * 0.6931471805599453f, e);   // not of infinities
+    if (fabsf(x) < 100.f) e = fmaf(e, r * kLn2, e);   // not of infinities
     e = fminf(e, 1e38f);
     const float d = 1.f + e, s = rcp_approx(d);
     return fmaf(s, fmaf(-d, s, 1.f), s);

@@ -604,3 +604,45 @@ def test_gate_over_its_range():
     want = x / (1 + np.exp(-x))
     tol = 2.0 ** -21 * np.abs(want) + np.abs(x) * 2.0 ** -126
     assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+
+
+@pytest.mark.parametrize("step", [False, True], ids=["prompt", "token"])
+def test_step_size_over_its_range(step):
+    """log(1 + e^x) of fp32 storage relative to its value: one token from an empty past with u = B_0 = C_0
+    = 1 and A = 0 gives it back.  U = 2^-24: the exponential's 4 U and 1 U for the factor that mends its
+    argument, 1 U for 2 + e, 2 U for its reciprocal, 1 U for their product, 1 U for the series and what
+    it leaves out, 0.5 U for its inner terms, 1 U for the last sum, so 12 U."""
+    D, N = 4096, 8
+    r = np.random.default_rng(41)
+    x = np.concatenate([np.linspace(-87, 95, 2048), r.uniform(-8, 4, 1024), r.uniform(-87, -20, 1024)])
+    x = x.astype(np.float32).astype(np.float64).reshape(1, 1, D)
+    one = np.zeros((1, 1, 1, N))
+    one[..., 0] = 1
+    d = [to_dev(a, "f32") for a in (np.ones((1, 1, D)), x, np.zeros((D, N)), one, one)]
+    with R.Ssm(D, N, 1, 2, "f32", 1, 1, training=False) as f:
+        if step:
+            got = f.scan_step(*(t[:, 0].contiguous() if i != 2 else t for i, t in enumerate(d)), f.new_state(1))
+        else:
+            got = f.scan(*d)
+    want = np.logaddexp(0, x)
+    tol = 12 * 2.0 ** -24 * want + 2.0 ** -126
+    err = np.abs(to_host(got).reshape(x.shape) - want)
+    assert (err <= tol).all(), (np.max(err / tol), x.flat[np.argmax(err / tol)])
+
+
+def test_step_size_of_infinities_and_nan():
+    """log(1 + e^x) at both infinities, at the type's lowest value, behind its last exponential and of a NaN."""
+    x = [float("inf"), float("-inf"), float("nan"), -3.4028234663852886e38, 3.4028234663852886e38, -128.5, 200.0, -1e4]
+    D, N = len(x), 8
+    for dtype in ("f32", "bf16"):
+        raw = torch.tensor(x, device="cuda").view(1, 1, D).to(torch.float32 if dtype == "f32" else torch.bfloat16)
+        one = torch.zeros(1, 1, 1, N, device="cuda", dtype=raw.dtype)
+        one[..., 0] = 1
+        with R.Ssm(D, N, 1, 2, dtype, 1, 1, training=False) as f:
+            got = f.scan(torch.ones_like(raw), raw, torch.zeros(D, N, device="cuda"), one, one)
+        got, raw = to_host(got).ravel(), to_host(raw).ravel()
+        # what the type holds: bf16 rounds fp32's largest numbers to infinities; an infinite step meets
+        # the zeros of B, which leaves no value
+        fin = raw < np.inf
+        assert np.isnan(got[np.isnan(raw)]).all() and not np.isfinite(got[raw == np.inf]).any()
+        np.testing.assert_array_equal(got[fin], np.maximum(raw, 0)[fin])
