@@ -184,8 +184,10 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvArgs a, int D, i
 // A run of R tokens is walked with the last K-1 inputs and gradients in
 // registers, g being formed again for the K-1 tokens behind the run ([8, 4096, 1536]
 // fp32: 112 us, 5.4 TB/s; 153 with the next rows in registers instead of the ring).
-// The run's sums of dw and dbias go to a row of the workspace, added in a fixed order
-// by k_conv_reduce.
+// The run's sums of dw and dbias go to a row of the workspace, added in a fixed order by
+// k_conv_reduce.  fp32 storage adds 4 tokens first: a term passes through R / 4 + rows / 64 +
+// 10 additions of fp32, R tokens a run.  16-bit storage adds them one by one: its gates are
+// good to 2^-19, and the additions in between cost 3% (80.3 to 82.6 us at [8, 4096, 1536]).
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads, conv_bwd_per_sm<T>())
 k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
@@ -221,6 +223,7 @@ k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
         }
     }
     constexpr int U = 4, STAGES = 3;   // tokens a step, steps in the ring
+    constexpr bool FOUR = sizeof(T) == 4;
     __shared__ Pack<T, V> ring[V > 1 ? STAGES : 1][2][U][kConvThreads];
     Pack<T, V> ahead[2][V > 1 ? 1 : U];
     const int tend = t0 < t1 ? min(len, t1 + K - 1) : t0;
@@ -258,13 +261,16 @@ k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
         if constexpr (V > 1) fetch(t4 + (STAGES - 1) * U, slot ? slot - 1 : STAGES - 1);
         else fetch(t4 + U, 0);
         slot = slot + 1 < STAGES ? slot + 1 : 0;
+        Pack<T, V> o[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int t = t4 + i;
-            const bool in = t < len, own = t < t1;
-            Pack<T, V> o;
+        for (int e = 0; e < V; ++e) {
+            float dw4[K], db4;   // of these tokens, or the run's sums themselves
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
+            for (int k = 0; k < K; ++k) dw4[k] = FOUR ? 0.f : dw[e][k];
+            db4 = FOUR ? 0.f : db[e];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const bool in = t4 + i < len, own = t4 + i < t1;
 #pragma unroll
                 for (int k = 0; k + 1 < K; ++k) { xs[e][k] = xs[e][k + 1]; gs[e][k] = gs[e][k + 1]; }
                 xs[e][K - 1] = to_f(rx[i].v[e]);
@@ -278,18 +284,24 @@ k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
                 if (!in) g = 0.f;
                 gs[e][K - 1] = g;
                 if (own) {
-                    db[e] += g;
+                    db4 += g;
 #pragma unroll
-                    for (int k = 0; k < K; ++k) dw[e][k] = fmaf(g, xs[e][k], dw[e][k]);
+                    for (int k = 0; k < K; ++k) dw4[k] = fmaf(g, xs[e][k], dw4[k]);
                 }
                 // dx of token t-K+1: taps k meet g[t-K+1 + K-1-k] = gs[K-1-k]
                 float s = 0.f;
 #pragma unroll
                 for (int k = 0; k < K; ++k) s = fmaf(w[e][k], gs[e][K - 1 - k], s);
-                from_f(o.v[e], s);
+                from_f(o[i].v[e], s);
             }
-            if (t - (K - 1) >= t0 && t - (K - 1) < t1)
-                *reinterpret_cast<Pack<T, V>*>(dx + (size_t)(t - (K - 1)) * D) = o;
+            db[e] = FOUR ? db[e] + db4 : db4;
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[e][k] = FOUR ? dw[e][k] + dw4[k] : dw4[k];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = t4 + i - (K - 1);
+            if (t >= t0 && t < t1) *reinterpret_cast<Pack<T, V>*>(dx + (size_t)t * D) = o[i];
         }
     }
     if constexpr (V > 1) copy_wait<0>();
@@ -302,24 +314,15 @@ k_conv_bwd(ConvArgs a, int D, int cblocks, int runs, int R, float* part) {
     }
 }
 
-// part [rows][K+1][D] summed over rows, in the rows' order within each of 8 lanes
-// and the lanes' order at the end.
+// part [rows][K+1][D] summed over rows in a fixed order.
 __global__ void __launch_bounds__(256) k_conv_reduce(const float* part, int rows, int D, int K, float* dweight,
                                                      float* dbias) {
-    __shared__ float s[8][33];
-    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int n = D * (K + 1), i = blockIdx.x * 32 + lane;
-    float acc = 0.f;
-    if (i < n)
-        for (int r = y; r < rows; r += 8) acc += part[(size_t)r * n + i];
-    s[y][lane] = acc;
-    __syncthreads();
-    if (y == 0 && i < n) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) acc += s[k][lane];
+    const int n = D * (K + 1), i = blockIdx.x * 32 + (threadIdx.x & 31);
+    const float sum = block_column_sum(i < n ? part + i : nullptr, n, rows);
+    if (threadIdx.x < 32 && i < n) {
         const int k = i / D, c = i % D;
-        if (k < K) dweight[(size_t)c * K + k] = acc;
-        else if (dbias) dbias[c] = acc;
+        if (k < K) dweight[(size_t)c * K + k] = sum;
+        else if (dbias) dbias[c] = sum;
     }
 }
 

@@ -646,3 +646,21 @@ def test_step_size_of_infinities_and_nan():
         fin = raw < np.inf
         assert np.isnan(got[np.isnan(raw)]).all() and not np.isfinite(got[raw == np.inf]).any()
         np.testing.assert_array_equal(got[fin], np.maximum(raw, 0)[fin])
+
+
+def test_convolution_sums_of_long_runs():
+    """dw and dbias of equal terms whose running fp32 sum rounds the same way at every step.  Runs of R =
+    500 tokens, B = 230 of them: with U = 2^-24 the four terms of a group cost 2.25 U of their sum, the
+    groups of a run half a U each, so (R / 4 + 1) / 2, the runs of one of 64 sums (B / 64 + 1) / 2, and
+    their six levels one U each."""
+    B, L, D, K = 230, 500, 512, 4
+    c = 1 + 128 * 2.0 ** -23
+    x, g = torch.ones(B, L, D, device="cuda"), torch.full((B, L, D), c, device="cuda")
+    w, b = torch.randn(D, K, device="cuda"), torch.zeros(D, device="cuda")
+    with R.Ssm(D, 8, 1, K, "f32", B, L) as f:
+        _, dw, db = f.conv_backward(x, w, g, b, silu=False)
+    tol = (2.25 + (L / 4 + 1) / 2 + (B / 64 + 1) / 2 + 6) * 2.0 ** -24
+    for k in range(K):
+        want = B * (L - (K - 1 - k)) * c
+        assert np.abs(to_host(dw[:, k]) / want - 1).max() <= tol
+    assert np.abs(to_host(db) / (B * L * c) - 1).max() <= tol
