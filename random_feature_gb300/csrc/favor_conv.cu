@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvArgs a, int D, i
 // registers, g being formed again for the K-1 tokens behind the run ([8, 4096, 1536]
 // fp32: 112 us, 5.4 TB/s; 153 with the next rows in registers instead of the ring).
 // The run's sums of dw and dbias go to a row of the workspace, added in a fixed order by
-// k_conv_reduce.  fp32 storage adds 4 tokens first: a term passes through R / 4 + rows / 64 +
-// 10 additions of fp32, R tokens a run.  16-bit storage adds them one by one: its gates are
+// k_conv_reduce.  fp32 storage adds 4 tokens first: a term passes through R / 4 + rows / 128 +
+// 11 additions of fp32, R tokens a run.  16-bit storage adds them one by one: its gates are
 // good to 2^-19, and the additions in between cost 3% (80.3 to 82.6 us at [8, 4096, 1536]).
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads, conv_bwd_per_sm<T>())

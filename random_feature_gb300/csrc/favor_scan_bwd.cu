@@ -533,26 +533,15 @@ __global__ void __launch_bounds__(256) k_bwd_bc(ScanArgs p, BwdPlan pl, BwdWs ws
     from_f(*o, s);
 }
 
-// Sums of the parameters' gradients over the chunks of every row.
+// Sums of the parameters' gradients over the chunks of every row, in a fixed order.
 __global__ void __launch_bounds__(256) k_bwd_params(ScanArgs p, BwdWs ws, int rows, int D, int N) {
-    __shared__ float s[8][33];
-    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const size_t DN = (size_t)D * N, all = DN + 2 * D, i = (size_t)blockIdx.x * 32 + lane;
+    const size_t DN = (size_t)D * N, all = DN + 2 * D, i = (size_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const float* src = i < DN ? ws.dA + i : i < DN + D ? ws.dskip + (i - DN) : ws.dbias + (i - DN - D);
-    const size_t step = i < DN ? DN : D;
-    float acc = 0.f;
-    if (i < all) {
-#pragma unroll 16
-        for (int r = y; r < rows; r += 8) acc += src[r * step];
-    }
-    s[y][lane] = acc;
-    __syncthreads();
-    if (y || i >= all) return;
-#pragma unroll
-    for (int k = 1; k < 8; ++k) acc += s[k][lane];
-    if (i < DN) p.dA[i] = acc;
-    else if (i < DN + D) { if (p.dskip) p.dskip[i - DN] = acc; }
-    else if (p.ddt_bias) p.ddt_bias[i - DN - D] = acc;
+    const float sum = block_column_sum(i < all ? src : nullptr, i < DN ? DN : D, rows);
+    if (threadIdx.x >= 32 || i >= all) return;
+    if (i < DN) p.dA[i] = sum;
+    else if (i < DN + D) { if (p.dskip) p.dskip[i - DN] = sum; }
+    else if (p.ddt_bias) p.ddt_bias[i - DN - D] = sum;
 }
 
 template <typename T, int N, int V>

@@ -227,37 +227,39 @@ __device__ __forceinline__ float sigmoid_f(float x) {
     return fmaf(s, fmaf(-d, s, 1.f), s);
 }
 
+// v[0..N) added two by two, N a power of two.
+template <int N>
+__device__ __forceinline__ float sum_two_by_two(float* v) {
+#pragma unroll
+    for (int n = N / 2; n > 0; n >>= 1)
+#pragma unroll
+        for (int k = 0; k < n; ++k) v[k] += v[k + n];
+    return v[0];
+}
 // For a block of 256 threads: lane l of every warp has a column, whose `rows` values lie `step`
-// floats apart from `at` on (null: none).  Warp 0's lanes get their sums.  Row r goes to the sum
-// of warp r % 8 and there to the (r / 8 % 8)-th of 8, which are added two by two: rows / 64 + 6
-// additions for a term, where one sum a warp has rows / 8.
+// floats apart from `at` on (null: none).  Warp 0's lanes get their sums.  Warp y has rows y, y + 8,
+// ..; 16 of them are loaded together and added two by two before they meet the warp's sum, so that a
+// term passes through rows / 128 + 7 additions.
 __device__ __forceinline__ float block_column_sum(const float* at, size_t step, int rows) {
-    constexpr int W = 8, P = 8;
+    constexpr int W = 8, P = 16;
     __shared__ float s[W][33];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-    float acc[P] = {};
+    float sum = 0.f, v[P];
     if (at) {
-        int r = y;
-        for (; r + W * (P - 1) < rows; r += W * P)
+        at += y * step;
+        step *= W;
+        for (int left = (rows - y + W - 1) / W; left > 0; left -= P) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) acc[k] += at[(r + W * k) * step];
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-            if (r + W * k < rows) acc[k] += at[(r + W * k) * step];
+            for (int k = 0; k < P; ++k, at += step) v[k] = k < left ? *at : 0.f;
+            sum += sum_two_by_two<P>(v);
+        }
     }
-    auto two_by_two = [](float* v) {
-#pragma unroll
-        for (int n = 4; n > 0; n >>= 1)
-#pragma unroll
-            for (int k = 0; k < n; ++k) v[k] += v[k + n];
-        return v[0];
-    };
-    s[y][lane] = two_by_two(acc);
+    s[y][lane] = sum;
     __syncthreads();
     if (y) return 0.f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) acc[k] = s[k][lane];
-    return two_by_two(acc);
+    for (int k = 0; k < W; ++k) v[k] = s[k][lane];
+    return sum_two_by_two<W>(v);
 }
 
 // Page of row b, or -1 if it is outside the pool (padding rows).

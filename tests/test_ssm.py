@@ -651,16 +651,30 @@ def test_step_size_of_infinities_and_nan():
 def test_convolution_sums_of_long_runs():
     """dw and dbias of equal terms whose running fp32 sum rounds the same way at every step.  Runs of R =
     500 tokens, B = 230 of them: with U = 2^-24 the four terms of a group cost 2.25 U of their sum, the
-    groups of a run half a U each, so (R / 4 + 1) / 2, the runs of one of 64 sums (B / 64 + 1) / 2, and
-    their six levels one U each."""
+    groups of a run half a U each, so (R / 4 + 1) / 2; of the runs' sums 16 meet in four levels, one U each,
+    the B / 128 of a warp cost (B / 128 + 1) / 2, and the eight warps meet in three levels."""
     B, L, D, K = 230, 500, 512, 4
     c = 1 + 128 * 2.0 ** -23
     x, g = torch.ones(B, L, D, device="cuda"), torch.full((B, L, D), c, device="cuda")
     w, b = torch.randn(D, K, device="cuda"), torch.zeros(D, device="cuda")
     with R.Ssm(D, 8, 1, K, "f32", B, L) as f:
         _, dw, db = f.conv_backward(x, w, g, b, silu=False)
-    tol = (2.25 + (L / 4 + 1) / 2 + (B / 64 + 1) / 2 + 6) * 2.0 ** -24
+    tol = (2.25 + (L / 4 + 1) / 2 + 4 + (B / 128 + 1) / 2 + 3) * 2.0 ** -24
     for k in range(K):
         want = B * (L - (K - 1 - k)) * c
         assert np.abs(to_host(dw[:, k]) / want - 1).max() <= tol
     assert np.abs(to_host(db) / (B * L * c) - 1).max() <= tol
+
+
+def test_parameter_sums_of_many_chunks():
+    """dskip of equal terms whose running fp32 sum rounds the same way at every step, over 16384 chunks of 32
+    tokens.  With U = 2^-24 a chunk's sum costs (32 + 1) / 2 U of it; 16 chunks meet in four levels, one U
+    each, the 16384 / 128 sums of a warp cost (128 + 1) / 2, and the eight warps meet in three levels."""
+    B, L, D, N = 8, 65536, 8, 8
+    c = 1 + 2557 * 2.0 ** -23
+    u = torch.full((B, L, D), c, device="cuda")
+    one, bc, A = torch.ones_like(u), torch.zeros(B, L, 1, N, device="cuda"), torch.zeros(D, N, device="cuda")
+    with R.Ssm(D, N, 1, 4, "f32", B, L) as f:
+        got = f.scan_backward(u, one, A, bc, bc, one, skip=torch.ones(D, device="cuda"))["dskip"]
+    tol = (16.5 + 4 + (B * L / 32 / 128 + 1) / 2 + 3) * 2.0 ** -24
+    assert np.abs(to_host(got) / (B * L * c) - 1).max() <= tol
