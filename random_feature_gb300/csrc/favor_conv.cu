@@ -354,12 +354,15 @@ static void conv_dispatch(const SsmHandle& h, bool vec, A... args) {
 
 static int conv_cblocks(int D, int V) { return (D + kConvThreads * V - 1) / (kConvThreads * V); }
 
-// Tokens a run so that the blocks come to whole waves of per_sm on every SM, with about
-// 128 tokens at most and `least` at least ([4, 8192, 1024] bf16 in runs of 72, one wave:
-// 30.7 us; of 32, 2.2 waves: 33.9).
+// Tokens a run so that the blocks come to whole waves of per_sm on every SM: as many waves as runs of
+// kConvRunTokens would take, and then as few tokens as that leaves, `least` at least ([4, 8192, 1024] bf16
+// in runs of 72, one wave: 30.7 us; of 32, 2.2 waves: 33.9).  The runs a row are rounded down, so that a
+// run has under 2 kConvRunTokens + U tokens.
+constexpr int kConvRunTokens = 256;
+
 static int run_tokens(const SsmHandle& h, int cb, int B, int L, int per_sm, int U, int least) {
     const long long slots = (long long)h.num_sms * per_sm, columns = (long long)cb * B;
-    const long long waves = (columns * L + slots * 256 - 1) / (slots * 256);
+    const long long waves = (columns * L + slots * kConvRunTokens - 1) / (slots * kConvRunTokens);
     long long runs = slots * waves / columns;
     if (runs < 1) runs = 1;
     long long R = (L + runs - 1) / runs;
@@ -402,10 +405,10 @@ struct ConvBwd {
 };
 
 // A row of partial sums a run.  run_tokens gives B rows (one run each) or slots * waves / cblocks at most,
-// and waves <= cblocks B L / (128 slots) + 1: together less than B + B L / 128 + slots.
+// and waves < cblocks B L / (kConvRunTokens slots) + 1: together less than B + B L / kConvRunTokens + slots.
 size_t conv_backward_ws(const SsmHandle& h) {
     const size_t slots = (size_t)h.num_sms * conv_bwd_per_sm<__nv_bfloat16>();   // the larger of the two
-    const size_t rows = (size_t)h.max_B * (1 + (h.max_L + 127) / 128) + slots;
+    const size_t rows = (size_t)h.max_B * (1 + (h.max_L + kConvRunTokens - 1) / kConvRunTokens) + slots;
     return rows * h.D * (h.K + 1);
 }
 

@@ -678,3 +678,72 @@ def test_parameter_sums_of_many_chunks():
         got = f.scan_backward(u, one, A, bc, bc, one, skip=torch.ones(D, device="cuda"))["dskip"]
     tol = (16.5 + 4 + (B * L / 32 / 128 + 1) / 2 + 3) * 2.0 ** -24
     assert np.abs(to_host(got) / (B * L * c) - 1).max() <= tol
+
+
+def _conv64(x, w, b):
+    """One row [n, D] in float64 on the device: (inputs with K-1 zeros before them, p, sum of the terms' magnitudes)."""
+    K = w.shape[1]
+    xp = torch.cat([x.new_zeros(K - 1, x.shape[1]), x]).double()
+    p, mag = b.double().expand(x.shape).clone(), b.double().abs().expand(x.shape).clone()
+    for k in range(K):
+        p += w[:, k].double() * xp[k:k + len(x)]
+        mag += (w[:, k].double() * xp[k:k + len(x)]).abs()
+    return xp, p, mag
+
+
+# on 152 SMs: runs of 504 tokens, one a row, in one wave of blocks; of 256, two a row, in two waves
+@pytest.mark.parametrize("B,L,D", [(115, 500, 2048), (8, 500, 56320)])
+def test_longest_runs(B, L, D):
+    """bf16; the last row is short."""
+    K, U = 4, 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(42)
+    x = torch.randn(B, L, D, device="cuda", generator=g).bfloat16()
+    w, b = torch.randn(D, K, device="cuda", generator=g), torch.randn(D, device="cuda", generator=g)
+    lens = [L] * (B - 1) + [L - 3]
+    with R.Ssm(D, 8, 1, K, "bf16", B, L, training=False) as f:
+        out = f.conv(x, w, b, lens=ints(lens))
+    for r in {0, B // 2, B - 1}:
+        n = lens[r]
+        _, p, mag = _conv64(x[r, :n], w, b)
+        want = p * torch.sigmoid(p)
+        # |silu'| <= 1.1; K + 1 fp32 operations on terms of size mag; the gate to 2^-18, and for |p| >= 16 to |p| 2^-22
+        tol = want.abs() * (2.0 ** -8 + 2.0 ** -18 + p.abs() * 2.0 ** -22) + 1.1 * mag * (K + 1) * U + 2.0 ** -120
+        assert ((out[r, :n].double() - want).abs() <= tol).all()
+        assert (out[r, n:] == 0).all()
+
+
+# runs of 500 tokens, one a row; of 252, two a row, in two waves of blocks
+@pytest.mark.parametrize("B,L,D", [(230, 500, 512), (8, 500, 28160)])
+def test_longest_runs_backward(B, L, D):
+    """fp32.  With s = sigmoid(p) good to 8 U of its value, s (1 + p (1 - s)) is off by 20 U (1 + |p|) at most, and
+    by silu'' <= 1/2 times p's own error; dx is K terms of it, dw and dbias sums of R / 4 + rows / 128 + 11 levels."""
+    K, U = 4, 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(43)
+    x, do = (torch.randn(B, L, D, device="cuda", generator=g) for _ in range(2))
+    w, b = torch.randn(D, K, device="cuda", generator=g), torch.randn(D, device="cuda", generator=g)
+    lens = [L] * (B - 1) + [L - 3]
+    with R.Ssm(D, 8, 1, K, "f32", B, L) as f:
+        dx, dw, db = f.conv_backward(x, w, do, b, lens=ints(lens))
+    want = torch.zeros(K + 1, D, device="cuda", dtype=torch.float64)
+    tol = torch.zeros_like(want)
+    levels = L / 4 + 2 * B / 128 + 11
+    for r, n in enumerate(lens):
+        xp, p, mag = _conv64(x[r, :n], w, b)
+        s = torch.sigmoid(p)
+        gr = do[r, :n].double() * (s * (1 + p * (1 - s)))
+        eg = do[r, :n].double().abs() * (20 * U * (1 + p.abs()) + 0.5 * (K + 1) * U * mag) + U * gr.abs()
+        d, ed = torch.zeros_like(p), torch.zeros_like(p)
+        for k in range(K):
+            at = K - 1 - k                          # dx[t] += w[k] g[t + at]
+            t = w[:, k].double() * gr[at:]
+            d[:n - at] += t
+            ed[:n - at] += (K + 1) * U * t.abs() + w[:, k].double().abs() * eg[at:]
+            term = gr * xp[k:k + n]
+            want[k] += term.sum(0)
+            tol[k] += levels * U * term.abs().sum(0) + (eg * xp[k:k + n].abs()).sum(0)
+        want[K] += gr.sum(0)
+        tol[K] += levels * U * gr.abs().sum(0) + eg.sum(0)
+        assert ((dx[r, :n].double() - d).abs() <= ed + U * d.abs()).all(), r
+        assert (dx[r, n:] == 0).all()
+    got = torch.cat([dw.t(), db[None]]).double()
+    assert ((got - want).abs() <= tol + U * want.abs()).all(), ((got - want).abs() / tol).max().item()
