@@ -131,3 +131,49 @@ def test_pages_of_a_serving_cache():
         R.pages_clear(state, _ints([new]))
         R.pages_clear(win, _ints([new]))
         both(slots + [new], alone + [(f.new_window(1), f.new_state(1))])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pages_of_favor_states(dtype):
+    """States [H, m, dv+1] of the stateful FAVOR+ calls as pages: sequences are decoded, one is forked, one is
+    freed, the live ones move together and are decoded on as the first pages of the pool; every sequence goes
+    on as it does alone.  Odd pages (65 columns), and odd rows of them."""
+    H, m, d, dv, P, T = 3, 32, 16, 64, 9, 5
+    r = np.random.default_rng(9)
+    omega = r.standard_normal((H, m, d)).astype(np.float32)
+    t = lambda n, w: torch.from_numpy((0.5 * r.standard_normal((n, H, T, w))).astype(np.float32)).cuda() \
+        .to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    with R.Favor(H, m, d, dv, "softmax_pos", dtype, omega, 0.5, P, 64) as f:
+        pool = f.new_state(P)
+        alone = [f.new_state(1) for _ in range(3)]
+
+        def both(n):
+            """T tokens of the first n pages, and of the same sequences alone."""
+            q, k, v = t(n, d), t(n, d), t(n, dv)
+            got = f.causal_step(q, k, v, pool[:n])
+            want = torch.cat([f.causal_step(q[i:i + 1], k[i:i + 1], v[i:i + 1], alone[i]) for i in range(n)])
+            assert torch.equal(got, want)
+            assert torch.equal(pool[:n], torch.cat(alone))
+        both(3)
+        both(3)
+        # sequence 2 forks into pages 8 and 5; sequence 0 ends
+        assert R.pages_copy(pool, pool, _ints([2, 2]), _ints([8, 5])).tolist() == [1, 1]
+        assert torch.equal(pool[8:9], alone[2]) and torch.equal(pool[5:6], alone[2])
+        table, n = R.pages_compact(pool, _ints([1, 2, 8, 5]))
+        assert n.item() == 4 and sorted(table.tolist()) == [0, 1, 2, 3]
+        seqs = [alone[1], alone[2], alone[2].clone(), alone[2].clone()]
+        alone = [None] * 4
+        for at, s in zip(table.tolist(), seqs):
+            alone[at] = s
+        both(4)
+        # a new sequence on a cleared page
+        R.pages_clear(pool, _ints([4]))
+        assert (pool[4] == 0).all()
+        alone.append(f.new_state(1))
+        both(5)
+        # the states of prompts, added up by the stateful call, in pages as well
+        k, v = t(1, d), t(1, dv)
+        one = f.kv_state(k, v)
+        assert R.pages_copy(pool, one, _ints([0]), _ints([7])).tolist() == [1] and torch.equal(pool[7:8], one)
+        q = t(1, d)
+        assert torch.equal(f.attn_from_state(q, pool[7:8]), f.attn_from_state(q, one))
