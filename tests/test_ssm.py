@@ -747,3 +747,31 @@ def test_longest_runs_backward(B, L, D):
         assert (dx[r, n:] == 0).all()
     got = torch.cat([dw.t(), db[None]]).double()
     assert ((got - want).abs() <= tol + U * want.abs()).all(), ((got - want).abs() / tol).max().item()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_slow_decays(dtype):
+    """Decays of 1e-5 to 1e-3 a token, whose errors add up over the whole row; through chunks, then through
+    single tokens, and the gradients of the row's start."""
+    B, L, D, N = 1, 3000, 16, 8
+    s = scan_inputs(B, L, D, N, 1, dtype, 44)
+    step = np.exp(np.random.default_rng(45).uniform(np.log(1e-5), np.log(1e-3), D))
+    s["raw"] = _round(0.1 * s["raw"], dtype)
+    s["dt_bias"] = np.log(np.expm1(step)).astype(np.float32).astype(np.float64)
+    s["A"] = -np.ones((D, N))
+    want, end = O.ssm_scan(**errs(s))
+    T = 700
+    part = {k: v[:, :T] if k in SEQ else v for k, v in s.items()}
+    g = _round(np.random.default_rng(46).standard_normal((B, T, D)), dtype)
+    grads = O.ssm_scan_backward(**errs(part), dout=Err(g))
+    with R.Ssm(D, N, 1, 4, dtype, B, L) as f:
+        d, state = dev(s, dtype), f.new_state(B)
+        head = {k: v[:, :L - 20].contiguous() if k in SEQ else v for k, v in d.items()}
+        outs = [call_scan(f, head, state=state)] + [call_step(f, d, t, state)[:, None] for t in range(L - 20, L)]
+        assert_within(to_host(torch.cat(outs, 1)), want, dtype)
+        assert_within(to_host(state), end, "f32")
+        p = dev(part, dtype)
+        got = f.scan_backward(p["u"], p["raw"], p["A"], p["Bm"], p["Cm"], to_dev(g, dtype), skip=p["skip"], z=p["z"],
+                              dt_bias=p["dt_bias"])
+        for k, w in grads.items():
+            assert_within(to_host(got[k]), w, dtype if k in ("du", "ddt", "dB", "dC", "dz") else "f32", k)
