@@ -176,7 +176,8 @@ def _made_on(stream, device, make):
     current = torch.cuda.current_stream(device)
     if raw == current.cuda_stream:
         return make()
-    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device)):
+    # (an external stream of address 0 would be one of torch's own streams)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)):
         made = make()
     for t in made if isinstance(made, tuple) else (made,):
         if t is not None:

@@ -59,7 +59,9 @@ def log(monkeypatch):
     for name in ("empty_like", "zeros_like", "empty", "zeros"):
         monkeypatch.setattr(torch, name, lambda *a, **k: _Made(log))
     monkeypatch.setattr(torch.cuda, "stream", current)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", _Stream)
+    # torch's takes the address 0 for "none given" and hands out one of its own streams
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, *a: _Stream(raw or 0x300))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: _Stream(0))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Stream(log.stack[-1]))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: log.stack[-1], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
@@ -116,6 +118,14 @@ def test_ssm_outputs_belong_to_the_given_stream(log, call, given):
     assert log.made and all(t.at == SIDE for t in log.made)
     assert len(log.calls) == 1 and log.calls[0][1][-1] == SIDE
     # the current stream may read them until they are freed
+    assert log.noted == [(t, CUR) for t in log.made]
+
+
+@pytest.mark.parametrize("given", [0, 1, _Stream(0)], ids=["address", "second-name", "object"])
+@pytest.mark.parametrize("call", SSM)
+def test_ssm_outputs_on_the_default_stream(log, call, given):
+    _ssm_calls(_ssm_object(log))[call](given)
+    assert log.made and all(t.at == 0 for t in log.made)
     assert log.noted == [(t, CUR) for t in log.made]
 
 
@@ -267,6 +277,29 @@ def test_favor_calls_beside_a_busy_stream(call):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("given", [0, 1, "object"])
+def test_calls_on_the_default_stream_beside_a_busy_current_one(given):
+    t = _gpu_case()
+    B, L, D = t["x"].shape
+    if given == "object":
+        given = torch.cuda.default_stream()
+    with R.Ssm(D, 16, 1, 4, "f32", B, L) as f:
+        run = lambda s: f.scan(f.conv(t["x"], t["w"], t["bias"], lens=t["lens"], stream=s), t["dt"], t["A"], t["Bm"],
+                               t["Cm"], lens=t["lens"], stream=s)
+        want = run(None).clone()
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            _busy()
+            _later_writes([(want.shape, want.dtype)])
+            got = run(given)
+            torch.cuda.default_stream().synchronize()
+            assert not side.query()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
 
 
 @pytest.mark.gpu
