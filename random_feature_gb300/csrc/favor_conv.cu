@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvArgs a, int D, i
 //     dx[t] = sum_k w[k] g[t + K - 1 - k],   dw[k] = sum_t g[t] x[t - K + 1 + k],   dbias = sum_t g[t]
 // A run of R tokens is walked with the last K-1 inputs and gradients in
 // registers, g being formed again for the K-1 tokens behind the run ([8, 4096, 1536]
-// fp32: 112 us, 5.4 TB/s; 153 with the next rows in registers instead of the ring).
+// fp32: 111 us, 5.4 TB/s; 153 with the next rows in registers instead of the ring).
 // The run's sums of dw and dbias go to a row of the workspace, added in a fixed order by
 // k_conv_reduce.  fp32 storage adds 4 tokens first: a term passes through R / 4 + rows / 128 +
 // 11 additions of fp32, R tokens a run.  16-bit storage adds them one by one: its gates are
@@ -356,7 +356,7 @@ static int conv_cblocks(int D, int V) { return (D + kConvThreads * V - 1) / (kCo
 
 // Tokens a run so that the blocks come to whole waves of per_sm on every SM: as many waves as runs of
 // kConvRunTokens would take, and then as few tokens as that leaves, `least` at least ([4, 8192, 1024] bf16
-// in runs of 72, one wave: 30.7 us; of 32, 2.2 waves: 33.9).  The runs a row are rounded down, so that a
+// in runs of 72, one wave, is 9% faster than in runs of 32, 2.2 waves).  The runs a row are rounded down, so that a
 // run has under 2 kConvRunTokens + U tokens.
 constexpr int kConvRunTokens = 256;
 

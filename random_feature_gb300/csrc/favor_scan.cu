@@ -18,18 +18,23 @@ enum { SCAN_OUT, SCAN_SUM, SCAN_GRAD };
 // channels of one group of one row, for one chunk of tokens walked in tiles of
 // TT.  A thread holds 8 states of 2 channels, LPC = N / 8 lanes a channel pair.
 //
-// What bounds it: at N = 16 a token of 32 channels (one warp's) takes 115
+// What bounds it: at N = 16 a token of 32 channels (one warp's) takes 110
 // instructions, 32 of them packed FMAs and MULs and 20 of the exponential unit.  On
 // this device an instruction's operands come from the registers two 32-bit words a
 // clock (measured: fma.f32x2 of three distinct operands issues every 3.1 clocks, of
 // two every 2.2, mul.f32x2 every 2.1, a plain fma 1.5, ex2 every 4.0), so the packed
-// ones take 85 clocks of a quarter SM, the exponentials 80, the issue 115; they
+// ones take 85 clocks of a quarter SM, the exponentials 80, the issue 110; they
 // overlap in part.  Measured with full waves: 150 clocks.  At [16, 512, 8192], us:
 // 328 so; without the exponentials 324, without the loads of B and C 314, without dt's
 // and the gate's functions 287 (they stood in a copy); one channel a thread, whose
 // lanes do not share the loads of B and C, 344; a token's decays formed between the
 // updates of the one before, 342; 5 blocks an SM in 102 registers, 342; 3 in 168,
 // 367; plain FMAs, 366.  Tokens a step of the walk: 8 against 4 is 2% faster.
+//
+// kScanPerSm, the blocks an SM that the registers allow, is also what the chunks are counted by.
+// Shared memory allows as many to SCAN_OUT for N = 8 and 16, and for N = 32 in fp32; in bf16 3 for
+// N = 32, and 2 for N = 64 in either type.  There the chunks come to two waves of blocks.  SCAN_GRAD
+// has 3, 3, 2 and 1 blocks an SM in bf16 for N = 8, 16, 32, 64, in fp32 4, 4, 3 and 2.
 constexpr int kScanNS = 8, kScanCH = 2, kScanPerSm = 4;
 
 struct ScanPlan {

@@ -32,8 +32,10 @@ constexpr int kBwdSub = 4;          // tokens whose states are in registers at a
 constexpr int kBwdTile = 16;        // tokens staged in shared memory at a time
 constexpr int kBwdNS = 4;           // states a thread, of
 constexpr int kBwdCH = 2;           // channels
-// Tokens of a chunk: the kept states take 4 KB for every 4 of them, and three blocks of 75 KB share an
-// SM (64 tokens and two blocks, before the states were formed a channel at a time: 4% slower).
+// Tokens of a chunk: the kept states take 4 KB for every 4 of them.  At N = 16 in bf16 three blocks of 74 KB
+// share an SM (64 tokens and two blocks, before the states were formed a channel at a time: 4% slower), at N =
+// 32 in either type too; fp32 at N = 16, bf16 at N = 8 and either at N = 64 have two (92 to 110 KB), fp32 at
+// N = 8 one (142 KB).
 constexpr int kBwdChunk = 32;
 
 struct BwdPlan {

@@ -141,10 +141,13 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // ex2.approx rounds towards smaller results: its mean relative error on this
-// device is -0.29 to -0.34 steps of 2^-24 for arguments in [-0.5, -0.001] (the
-// decays with a long memory, whose errors add up over it).  Exponents carry this
-// offset, 0.32 * 2^-24 * log2 e, which cancels the mean; an exponent of 0 still
-// gives 1.  Without it dA of a 777-token scan in fp32 is 1.3e-6 off instead of 6e-7.
+// device is -0.32 to -0.35 steps of 2^-24 for exponents in [-0.5, -0.003], where most
+// decays lie.  Exponents carry this offset, 0.32 * 2^-24 * log2 e, which leaves -0.03 to
+// 0.03 there; an exponent of 0 still gives 1.  Without it dA of a 777-token scan in fp32
+// is 1.3e-6 off instead of 6e-7.  Between -0.003 and -1e-7 the mean is -0.09 to -0.18
+// without the offset and 0.14 to 0.23 with it, about that of expf (0.26): at an exponent
+// of -r a token that comes to 0.2 * 2^-24 / r of a long memory.  Half the offset has
+// -0.02 to 0.07 there, and -0.16 to -0.25 in the range above.  Below -0.5 an offset is lost.
 constexpr float kEx2Mean = 2.75e-8f;
 
 // Two floats in one 64-bit register pair: the packed FMA / MUL issue two states'
