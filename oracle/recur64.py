@@ -2,7 +2,8 @@
 NumPy -- the oracle.
 
 TEST INFRASTRUCTURE, like ssm64.py: token by token from the definitions; the numeric functions take NumPy
-arrays, or array-likes with the same indexing and arithmetic that carry a rounding-error bound.
+arrays, or array-likes with the same indexing and arithmetic that carry a rounding-error bound.  (a h rather than
+h - c h, so that a bound on h's error shrinks with h: |a| e, not (1 + c) e, which grows past any use in a long row.)
 
     recurrence  s = sigmoid(r + r_bias),  a = e^(-rate s)  (a = s without a rate),  w = 1, 1 - a or
                 sqrt(1 - a^2),  h <- a h + w sigmoid(i + i_bias) x,  out = h z sigmoid(z)
@@ -68,7 +69,7 @@ def recurrence(x, r, i=None, rate=None, r_bias=None, i_bias=None, z=None, scale=
         for t in range(n):
             _, _, c, w, _ = _gates(r[b, t], rate, r_bias, scale)
             _, _, v = _input(x[b, t], _row(i, b, t), i_bias)
-            h = h + (w * v - c * h)
+            h = (1.0 - c) * h + w * v
             out[b, t] = h if z is None else h * (z[b, t] * _sigmoid(z[b, t]))
         end[b] = h
     return out, end
@@ -84,7 +85,7 @@ def recurrence_backward(x, r, dout, i=None, rate=None, r_bias=None, i_bias=None,
         for t in range(n):
             _, _, c, w, _ = _gates(r[b, t], rate, r_bias, scale)
             _, _, v = _input(x[b, t], _row(i, b, t), i_bias)
-            hs.append(hs[-1] + (w * v - c * hs[-1]))
+            hs.append((1.0 - c) * hs[-1] + w * v)
         mu = _zeros(x, (D,))                                      # a lambda of the token behind
         for t in reversed(range(n)):
             s, sn, c, w, rw = _gates(r[b, t], rate, r_bias, scale)
@@ -95,7 +96,7 @@ def recurrence_backward(x, r, dout, i=None, rate=None, r_bias=None, i_bias=None,
                 g["dz"][b, t] = up * hs[t + 1] * (zs * (1.0 + z[b, t] * zn))
                 up = up * (z[b, t] * zs)
             lam = up + mu
-            mu = lam - c * lam
+            mu = a * lam
             g["dx"][b, t] = lam * w * si
             if i is not None:
                 g["di"][b, t] = lam * w * v * sin
