@@ -63,8 +63,9 @@ struct RecurChan {
 };
 
 // A token's decay a is kept as d: where 0 <= 1 - a < 1/2, d = -(1 - a), and a h + b is h + (d h + b); else d = a
-// (0 or more), and it is d h + b.  Next to 1, fp32 holds 1 - a to many more digits than a, which would be
-// 2^-25 off at every token, 2^-25 / (1 - a) of a state that lives 1 / (1 - a) tokens.  SLOW: the first kind alone.
+// (+0 or more), and it is d h + b.  d's sign bit tells them apart, so a token that loses nothing has -0.  Next to 1,
+// fp32 holds 1 - a to many more digits than a, which would be 2^-25 off at every token, 2^-25 / (1 - a) of a state
+// that lives 1 / (1 - a) tokens.  SLOW: the first kind alone.
 template <bool SLOW>
 __device__ __forceinline__ F2 recur_next(F2 d, F2 h, F2 b) {
     const F2 t = fma2(d, h, b);
@@ -99,7 +100,7 @@ __device__ __forceinline__ void any_decay(float y, float& c, float& d, float& a)
     const float e = ex2_approx(-y * kLog2e);
     c = fabsf(y) < 0.35f ? y * p : 1.f - e;
     const bool near = c >= 0.f && c < 0.5f;
-    d = near ? -c : e;
+    d = near ? -fabsf(c) : e;      // a rate of -0, or one below 0 under a closed gate, makes c a -0
     a = near ? 1.f - c : e;
 }
 
