@@ -71,7 +71,7 @@ __device__ __forceinline__ void activate(int act, const F2 (&x)[N], F2 (&f)[N], 
             if (GRAD) sigmoids2<T>(y, none, s, sn);
             else s = sigmoid2<T>(y, none);
             f[i] = x[i] * s;
-            if (GRAD) {     // an x^2 past all bounds meets a sn of 0
+            if (GRAD) {     // an x^2 past all bounds meets a sn (x > 0) or an s of 0
                 const F2 q = each(xx, [](float v) { return fminf(v, 1e30f); });
                 df[i] = fma2(f[i] * sn, fma2(q, both(6.f * kGeluC * kGeluK), both(2.f * kGeluC)), s);
             }

@@ -50,17 +50,20 @@ __device__ __forceinline__ F2 sigmoid2(F2 x, F2 bias) {
     }
     return each(x + bias, [](float v) { float s, n; sigmoids<T>(v, s, n); return s; });
 }
-// sigmoid(x) and sigmoid(-x) = e sigmoid(x), e = e^-x, which is kept finite for it (but a NaN, a NaN).
-template <typename T>
+// sigmoid(x) and sigmoid(-x) = e sigmoid(x), e = e^-x, which is kept finite for it (but a NaN, a NaN).  sigmoid(x) itself
+// is 0 from there on, as a product with an x of the type's lowest value has to be (2^-126 makes -4 of bf16's).  KEPT:
+// 2^-126 stays, for a decay, whose state is nowhere near 2^126 (the recurrence without rates is 3% slower with the 0).
+template <typename T, bool KEPT = false>
 __device__ __forceinline__ void sigmoids2(F2 x, F2 bias, F2& s, F2& sn) {
     if (sizeof(T) == 2) {
-        const F2 e = each(fma2(x, both(-kLog2e), bias), [](float t) {
+        const F2 t = each(fma2(x, both(-kLog2e), bias), [](float v) {
             float m;
-            asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(m) : "f"(t));      // 126
-            return ex2_approx(m);
+            asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(m) : "f"(v));      // 126
+            return m;
         });
-        s = each(e + both(1.f), [](float d) { return rcp_approx(d); });
-        sn = e * s;
+        const F2 e(ex2_2(t.v)), r = each(e + both(1.f), [](float d) { return rcp_approx(d); });
+        sn = e * r;
+        s = KEPT ? r : F2(t.x() >= 126.f ? 0.f : r.x(), t.y() >= 126.f ? 0.f : r.y());
         return;
     }
     const F2 raw = x + bias;

@@ -107,7 +107,7 @@ __device__ __forceinline__ void any_decay(float y, float& c, float& d, float& a)
 template <typename T, bool RATE, int SCALE, bool SLOW, bool GRAD>
 __device__ __forceinline__ RecurGate recur_gate(F2 r, const RecurChan& p) {
     RecurGate g;
-    if (!RATE || GRAD) sigmoids2<T>(r, p.r_bias, g.s, g.sn);
+    if (!RATE || GRAD) sigmoids2<T, true>(r, p.r_bias, g.s, g.sn);
     else g.s = sigmoid2<T>(r, p.r_bias);
     if (SLOW) {
         // -c by the series to y^5/5!, the rest of which is under 0.125^5 / 6! = 4e-8 of it
