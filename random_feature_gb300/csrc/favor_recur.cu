@@ -38,7 +38,8 @@ __global__ void __launch_bounds__(kRecThreads, kRecPerSm) k_recur_maps(RecurArgs
         if (warp == 0 && page >= 0) first[((size_t)b * at.p.slabs + slab) * 32 + lane] = load_vec(a.state + (size_t)page * D, l);
     }
     const int t0 = (chunk * kRecWarps + warp) * at.p.run, end = min(len, t0 + at.p.run);
-    RecurMap m = no_map();
+    F4 mh = {both(0.f), both(0.f)};     // the run's map: its decays' product, and its state from an empty start
+    RunDecay ma, mb;
     if (t0 < end) {
         const size_t row0 = (size_t)b * a.L * D;
         const T *x = (const T*)a.x + row0, *r = (const T*)a.r + row0, *gi = (const T*)a.i + row0;
@@ -47,13 +48,17 @@ __global__ void __launch_bounds__(kRecThreads, kRecPerSm) k_recur_maps(RecurArgs
             constexpr bool SLOW = decltype(slow)::value;
             RecurMaps<T> q;
             group_gates<T, RATE, SCALE, SLOW, decltype(whole)::value>(vx, vr, vi, a.i, par, t, end, q);
-            RecurMap g = no_map();
+            F4 h = {both(0.f), both(0.f)};
+            GroupDecay<SLOW> ga, gb;
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                g.h = next4<SLOW>(q.d[s], g.h, q.in[s]);
-                g.p = scale4<SLOW>(q.d[s], g.p);
+                h = next4<SLOW>(q.d[s], h, q.in[s]);
+                ga.token(q.d[s].a);
+                gb.token(q.d[s].b);
             }
-            m = join(g, m);
+            mh = {ma.apply(h.a, mh.a), mb.apply(h.b, mh.b)};
+            ma.join(ga);
+            mb.join(gb);
         };
         int t = t0 + (end - 1 - t0) / G * G;
         const int whole = l.quads ? (end - t0) / G * G : 0;     // tokens of whole groups, read 4 channels at a time
@@ -83,6 +88,7 @@ __global__ void __launch_bounds__(kRecThreads, kRecPerSm) k_recur_maps(RecurArgs
             else walk(std::false_type());
         }
     }
+    RecurMap m = {{ma.value(), mb.value()}, mh};
     *at.run_at(b, chunk, warp, slab) = m;
     runs[warp][lane] = m;
     __syncthreads();

@@ -40,7 +40,9 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
     const RecurLane l(a, D, slab);
     const int len = row_len(a.lens, b, a.L);
     const int t0 = (chunk * kRecWarps + warp) * p.run, end = min(len, t0 + p.run);
-    RecurMap m = no_map(), back = no_map();
+    const F4 none = {both(0.f), both(0.f)};
+    F4 mh = none, back = none;      // the run's maps: the decays' product serves both
+    RunDecay ma, mb;
     if (t0 < end) {
         const size_t row0 = (size_t)b * a.L * D;
         const T *x = (const T*)a.x + row0, *r = (const T*)a.r + row0, *gi = (const T*)a.i + row0, *z = (const T*)a.z + row0;
@@ -50,14 +52,16 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
             constexpr bool SLOW = decltype(slow)::value;
             RecurMaps<T> q;
             group_gates<T, RATE, SCALE, SLOW, decltype(whole)::value>(vx, vr, vi, a.i, par, t, end, q);
-            *groups(p, b, chunk, warp, (t - t0) / G, slab) = m;
-            RecurMap g = no_map(), gb = no_map();
+            const F4 before = {ma.value(), mb.value()};
+            *groups(p, b, chunk, warp, (t - t0) / G, slab) = {before, mh};
+            F4 h = none, hb = none;
+            GroupDecay<SLOW> ga, gb;
 #pragma unroll
             for (int s = 0; s < G; ++s) {
-                g.h = next4<SLOW>(q.d[s], g.h, q.in[s]);
-                g.p = scale4<SLOW>(q.d[s], g.p);
+                h = next4<SLOW>(q.d[s], h, q.in[s]);
+                ga.token(q.d[s].a);
+                gb.token(q.d[s].b);
             }
-            gb.p = g.p;
             F4 up[G];
 #pragma unroll
             for (int s = 0; s < G; ++s) up[s] = vg(s);
@@ -71,10 +75,12 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
 #pragma unroll
             for (int s = G - 1; s >= 0; --s) {
                 if (!decltype(whole)::value && t + s >= end) continue;
-                gb.h = scale4<SLOW>(q.d[s], {gb.h.a + up[s].a, gb.h.b + up[s].b});
+                hb = scale4<SLOW>(q.d[s], {hb.a + up[s].a, hb.b + up[s].b});
             }
-            m = join(m, g);
-            back = join(gb, back);
+            mh = {ga.apply(mh.a, h.a), gb.apply(mh.b, h.b)};
+            back = {fma2(before.a, hb.a, back.a), fma2(before.b, hb.b, back.b)};
+            ma.join(ga);
+            mb.join(gb);
         };
         int t = t0;
         const int whole = l.quads ? t0 + (end - t0) / G * G : t0;
@@ -108,10 +114,13 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
             group(std::false_type(), std::false_type(), t, vx, vr, vi, vz, vg);
         }
     }
+    const F4 product = {ma.value(), mb.value()};
+    RecurMap m = {product, mh};
+    const RecurMap handed = {product, back};
     *fwd.run_at(b, chunk, warp, slab) = m;
-    *rev.run_at(b, chunk, warp, slab) = back;
+    *rev.run_at(b, chunk, warp, slab) = handed;
     runs[0][warp][lane] = m;
-    runs[1][warp][lane] = back;
+    runs[1][warp][lane] = handed;
     __syncthreads();
     if (warp == 0) {
         m = runs[0][0][lane];

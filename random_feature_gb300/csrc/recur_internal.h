@@ -356,6 +356,44 @@ __device__ __forceinline__ RecurMap join(const RecurMap& first, const RecurMap& 
     return {{first.p.a * then.p.a, first.p.b * then.p.b}, apply(then, first.h)};
 }
 
+// Products of decays.  Equal decays next to 1 (an open gate's) round the same way at every token: their product kept in
+// one float drifts by half a step a token, 5e-5 of a state in runs of 1024 tokens.  So a group's is kept as its loss,
+// p - 1 (SLOW), or in two floats, p + rest; a run's in two.
+template <bool SLOW>
+struct GroupDecay {
+    F2 p, rest;
+    __device__ __forceinline__ GroupDecay() : p(both(SLOW ? 0.f : 1.f)), rest(both(0.f)) {}
+    __device__ __forceinline__ void token(F2 d) {
+        if (SLOW) {
+            p = p + fma2(d, p, d);
+            return;
+        }
+        // the rest of a product with a decay next to 1; one below 1/2 halves the product, and keeps none
+        const bool kx = __float_as_int(d.x()) < 0, ky = __float_as_int(d.y()) < 0;
+        const F2 keep(kx ? p.x() : 0.f, ky ? p.y() : 0.f), next = fma2(d, p, keep);
+        const F2 sum = rest + fma2(d, p, fma2(next, both(-1.f), keep));
+        p = next;
+        rest = F2(kx ? sum.x() : 0.f, ky ? sum.y() : 0.f);
+    }
+    // (the product) x + h
+    __device__ __forceinline__ F2 apply(F2 x, F2 h) const {
+        return SLOW ? x + fma2(p, x, h) : fma2(p, x, fma2(rest, x, h));
+    }
+};
+struct RunDecay {
+    F2 p, rest;
+    __device__ __forceinline__ RunDecay() : p(both(1.f)), rest(both(0.f)) {}
+    __device__ __forceinline__ F2 value() const { return p + rest; }
+    __device__ __forceinline__ F2 apply(F2 x, F2 h) const { return fma2(p, x, fma2(rest, x, h)); }
+    template <bool SLOW>
+    __device__ __forceinline__ void join(const GroupDecay<SLOW>& g) {
+        const F2 minus = both(-1.f), next = SLOW ? fma2(p, g.p, p) : p * g.p;
+        const F2 err = fma2(p, g.p, SLOW ? fma2(next, minus, p) : next * minus);
+        rest = SLOW ? fma2(rest, g.p, rest) + err : fma2(rest, g.p, fma2(p, g.rest, err));
+        p = next;
+    }
+};
+
 // The maps of a call's runs and chunks, in the workspace: [row][chunk][run][slab] and [row][chunk][slab] of a warp's lanes.
 struct RecurMapsAt {
     RecurMap *run, *chunk;

@@ -46,3 +46,38 @@ def test_decays_of_one(rates, D, scale, dtype):
         assert_within(to_host(state), end, "f32", "state behind the steps")
         check_grads(f.backward(**d, dout=to_dev(g, dtype)), O.recurrence_backward(**errs(s), dout=Err(g), scale=scale),
                     dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rates", [[1e-6, 1e-5, 1e-4, 1e-3], [1e-6, 0.5, 1e-4, 1e-5, 2.0, 1e-3, 3e-6, 1e-2]],
+                         ids=["slow", "beside_fast"])
+def test_equal_decays_in_long_runs(rates, dtype):
+    """Open gates give a channel the same decay at every token.  Over runs of 1024 tokens (160 rows, so that a row is
+    cut into 8) what rounding leaves must not add up: a decay of 1 - 17.5 steps of fp32 that is kept as 1 - 17 or 18
+    steps would."""
+    B, L, D = 160, 8192, len(rates)
+    r = np.random.default_rng(33)
+    x = _round(np.abs(r.standard_normal((B, L, D))), dtype)
+    g = _round(np.abs(r.standard_normal((B, L, D))), dtype)
+    rate = np.array(rates, np.float32).astype(np.float64)
+    a = np.exp(-rate)
+    hs, lam = np.zeros((L + 1, B, D)), np.zeros((L + 1, B, D))
+    for t in range(L):
+        hs[t + 1] = a * hs[t] + x[:, t]
+    for t in reversed(range(L)):
+        lam[t] = g[:, t] + a * lam[t + 1]
+    drate = -np.sum(a * lam[:L] * hs[:L], (0, 1))
+    # All terms are positive, and independent roundings, uniform within half a step (2^-24 of the value, deviation
+    # 2^-24 / sqrt 3), come to sqrt(L / 3) 2^-24 = 3.1e-6 in L tokens: five of it.  drate has the states', the
+    # gradients' and its own sum's.
+    near = 5 * np.sqrt(L / 3) * 2.0 ** -24
+    with R.Recurrence(D, dtype, B, L, "plain") as f:
+        d = dict(x=to_dev(x, dtype), r=to_dev(np.full((B, L, D), 40.0), dtype), rate=to_dev(rate, "f32"))
+        state = f.new_state(B)
+        out = to_host(f.scan(**d, state=state))
+        assert np.abs(to_host(state) / hs[L] - 1).max() <= near
+        got = f.backward(**d, dout=to_dev(g, dtype))
+        assert np.abs(to_host(got["drate"]) / drate - 1).max() <= 3 * near
+        if dtype == "f32":
+            assert np.abs(out / hs[1:].transpose(1, 0, 2) - 1).max() <= near
+            assert np.abs(to_host(got["dx"]) / lam[:L].transpose(1, 0, 2) - 1).max() <= near
