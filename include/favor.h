@@ -457,7 +457,9 @@ FAVOR_API favor_status favor_ssm_scan_backward(favor_ssm h, const void* u, const
  * z, out and dout are [B, L, D] of the handle's dtype; rate (in general positive:
  * below 0 the state grows, and has no value once its growth over a row's tokens
  * passes fp32), r_bias and i_bias DEVICE float [D]; i, z, rate, r_bias and i_bias may be NULL
- * (i_bias only with i).  A state is a page [D] of float.  Arithmetic, states and
+ * (i_bias only with i).  A state is a page [D] of float; one that is not finite (or an
+ * input that makes it so) leaves its channel's row NaN or infinite from there on,
+ * NaN also where a h + b would stay infinite.  Arithmetic, states and
  * sums are fp32; outputs are rounded once.  The favor_conv_causal calls are the
  * convolution in front, the favor_pages calls serve its states.
  */

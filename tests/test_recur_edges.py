@@ -81,3 +81,35 @@ def test_equal_decays_in_long_runs(rates, dtype):
         if dtype == "f32":
             assert np.abs(out / hs[1:].transpose(1, 0, 2) - 1).max() <= near
             assert np.abs(to_host(got["dx"]) / lam[:L].transpose(1, 0, 2) - 1).max() <= near
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 5, 300])
+def test_states_that_are_not_finite(L, dtype):
+    """An infinite or NaN state stays out of reach, in its own channel and row; rows without tokens leave theirs alone."""
+    B, D = 3, 12
+    s = inputs(B, L, D, dtype, 34)
+    h0 = np.random.default_rng(35).standard_normal((B, D)).astype(np.float32)
+    bad = h0.copy()
+    bad[0, 3], bad[0, 8], bad[1, 0], bad[2, 1] = np.inf, np.nan, -np.inf, np.inf
+    lens = [L, L, 0]
+    want = O.recurrence(**errs(s), state=Err(h0), lens=lens)[0]
+    reached = np.zeros((B, D), bool)
+    reached[0, [3, 8]] = reached[1, 0] = True
+    with R.Recurrence(D, dtype, B, L) as f:
+        d = dev(s, dtype)
+        state = torch.from_numpy(bad).cuda()
+        out = f.scan(**d, state=state, lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        outs = [(to_host(out), to_host(state))]
+        if L == 1:
+            state = torch.from_numpy(bad).cuda()
+            pages = torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda")
+            out = f.step(**{k: v[:, 0].contiguous() if k in SEQ else v for k, v in d.items()}, state=state, pages=pages)
+            outs.append((to_host(out[:, None]), to_host(state)))
+        lost = np.broadcast_to(reached[:, None], (B, L, D))
+        want = Err(np.where(lost, 0, want.v), want.e)
+        for got, st in outs:
+            assert not np.isfinite(got[lost]).any()
+            assert_within(np.where(lost, 0, got), want, dtype)
+            assert (np.isfinite(st) == (np.isfinite(bad) & ~reached)).all()
+            assert np.array_equal(st[2], bad[2].astype(np.float64))
