@@ -472,11 +472,12 @@ typedef struct favor_recur_s* favor_recur;
 
 /*
  * favor_recur_create -- a handle for D channels (up to 2^20); max_B*max_L and
- * max_B*D up to 2^30, max_B*max_L*D up to 2^36.  Its workspace takes 9 KB for each
- * of 2 blocks an SM (or for every 128 channels of every row, if these are more) and
- * 4 bytes for every row and channel;
- * training != 0 adds as much again and 2 bytes (fp32: 4) for every token and
- * channel, for favor_recur_backward, which gives FAVOR_ERR_UNSUPPORTED without.
+ * max_B*D up to 2^30, max_B*max_L*D up to 2^36.  Its workspace: with
+ * R = max_B * ceil(D / 128) and N the larger of R and min(2 SMs, R * min(64,
+ * ceil(max_L / 64))), 9216 * N + 512 * R bytes, none where max_L <= 8.  training != 0
+ * makes it 19968 * N + 1024 * R * ceil(max_L / 4) bytes (fp32: max_L / 2) where that
+ * is more (2 bytes, fp32 4, for every token and channel, D rounded up to 128), for
+ * favor_recur_backward, which gives FAVOR_ERR_UNSUPPORTED without.
  * favor_recur_destroy frees it (after synchronising its device); accepts NULL.
  */
 FAVOR_API favor_status favor_recur_create(favor_recur* out, int D, favor_recur_scale scale, favor_dtype dtype,

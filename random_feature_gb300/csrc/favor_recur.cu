@@ -236,9 +236,10 @@ struct RecurStep {
     }
 };
 
-// The maps of runs and chunks, and the rows' starts.
+// The maps of runs and chunks, and the rows' starts; nothing where every row is one run.
 size_t recur_scan_ws(const RecurHandle& h) {
-    return recur_blocks_max(h.num_sms, kRecPerSm, h.D, h.max_B) * (kRecWarps + 1) * kRecMapFloats +
+    if (h.max_L <= kRecRunMin) return 0;
+    return recur_blocks_max(h.num_sms, kRecPerSm, h.D, h.max_B, h.max_L) * (kRecWarps + 1) * kRecMapFloats +
            (size_t)h.max_B * ((h.D + kRecSlab - 1) / kRecSlab) * 32 * (sizeof(F4) / 4);
 }
 

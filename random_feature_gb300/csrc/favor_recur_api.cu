@@ -80,7 +80,8 @@ favor_status favor_recur_create(favor_recur* out, int D, favor_recur_scale scale
     if (h->num_sms < 1) h->num_sms = 1;
     h->ws_floats = recur_scan_ws(*h);
     if (h->training && recur_backward_ws(*h) > h->ws_floats) h->ws_floats = recur_backward_ws(*h);
-    const cudaError_t e = cudaMalloc(&h->ws, h->ws_floats * sizeof(float));
+    h->ws = nullptr;
+    const cudaError_t e = h->ws_floats ? cudaMalloc(&h->ws, h->ws_floats * sizeof(float)) : cudaSuccess;
     if (e != cudaSuccess) {
         const favor_status st = e == cudaErrorMemoryAllocation ? FAVOR_ERR_NOMEM : FAVOR_ERR_CUDA;
         set_error(st, "%s: cudaMalloc of %zu bytes: %s", fn, h->ws_floats * sizeof(float), cudaGetErrorString(e));
@@ -99,7 +100,7 @@ favor_status favor_recur_destroy(favor_recur hd) {
     cudaGetDevice(&cur);
     if (cur != h->device) cudaSetDevice(h->device);
     cudaDeviceSynchronize();
-    cudaFree(h->ws);
+    if (h->ws) cudaFree(h->ws);
     if (cur != h->device) cudaSetDevice(cur);
     delete h;
     cudaGetLastError();

@@ -19,12 +19,12 @@ namespace favor {
 // (capped at 128 it spills: 312 us; its rows through shared memory then 261; chunks for one block an SM 277).
 constexpr int kRecBwdPerSm = 2;
 
-// The maps from a run's start to its groups: [row][chunk][run][group][slab] of a warp's lanes.
+// The maps from a run's start to its groups: [row][group of the row][slab] of a warp's lanes.
 struct GroupMapsAt {
     RecurMap* at;
-    int groups;     // of a run
-    __device__ __forceinline__ RecurMap* operator()(const RecurPlan& p, int b, int chunk, int w, int g, int slab) const {
-        return at + (((((size_t)b * p.chunks + chunk) * kRecWarps + w) * groups + g) * p.slabs + slab) * 32 + (threadIdx.x & 31);
+    int groups;     // of a row
+    __device__ __forceinline__ RecurMap* operator()(const RecurPlan& p, int b, int g, int slab) const {
+        return at + (((size_t)b * groups + g) * p.slabs + slab) * 32 + (threadIdx.x & 31);
     }
 };
 
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
             RecurMaps<T> q;
             group_gates<T, RATE, SCALE, SLOW, decltype(whole)::value>(vx, vr, vi, a.i, par, t, end, q);
             const F4 before = {ma.value(), mb.value()};
-            *groups(p, b, chunk, warp, (t - t0) / G, slab) = {before, mh};
+            *groups(p, b, t / G, slab) = {before, mh};
             F4 h = none, hb = none;
             GroupDecay<SLOW> ga, gb;
 #pragma unroll
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kRecThreads, 1) k_recur_bwd(RecurArgs a, int D
         const RecurChan4 par = load_chans<T>(a, l);
         auto group = [&](auto slow, auto whole, int t, auto vx, auto vr, auto vi, auto vz, auto vg) {
             constexpr bool SLOW = decltype(slow)::value, WHOLE = decltype(whole)::value;
-            const F4 h0 = apply(*groups(p, b, chunk, warp, (t - t0) / G, slab), start);
+            const F4 h0 = apply(*groups(p, b, t / G, slab), start);
             typedef typename Raw4<T>::H H;
             H ox[2][G], orr[2][G], oi[2][G], oz[2][G];
             // one pair of channels after the other: both at once take more registers than two blocks an SM leave
@@ -297,6 +297,8 @@ __global__ void __launch_bounds__(256) k_recur_reduce(const float* part, int row
 }
 
 // ------------------------------------------------------------------ host
+static int recur_groups(int L, int group) { return L / group + (L % group != 0); }
+
 template <typename T, bool RATE, int SCALE>
 struct RecurBwd {
     static void go(const RecurHandle& h, const RecurArgs& a, cudaStream_t st) {
@@ -314,8 +316,8 @@ struct RecurBwd {
         fwd.chunk = take(chunk);
         rev.chunk = take(chunk);
         GroupMapsAt groups;
-        groups.groups = fwd.p.run / rec_group<T>();
-        groups.at = take(run * groups.groups);
+        groups.groups = recur_groups(a.L, rec_group<T>());
+        groups.at = take((size_t)a.B * groups.groups * fwd.p.slabs * kRecMapFloats);
         const int rows = a.B * fwd.p.chunks;
         const unsigned blocks = (unsigned)rows * fwd.p.slabs;
         k_recur_bwd_maps<T, RATE, SCALE><<<blocks, kRecThreads, 0, st>>>(a, h.D, fwd, rev, groups);
@@ -328,14 +330,13 @@ struct RecurBwd {
     }
 };
 
-// Two sets of maps, three sums a channel for every chunk of a row, and a map for every group: runs and chunks cover
-// less than L + kRecWarps * run tokens of a row, with a run of (L / runs) + kRecGroupMax or kRecRunMin tokens.
+// Two sets of maps, three sums a channel for every chunk of a row, and a map for every group.
 size_t recur_backward_ws(const RecurHandle& h) {
-    const size_t blocks = recur_blocks_max(h.num_sms, kRecBwdPerSm, h.D, h.max_B);
-    const size_t group = h.dtype == FAVOR_DTYPE_F32 ? rec_group<float>() : rec_group<__nv_bfloat16>();
+    const size_t blocks = recur_blocks_max(h.num_sms, kRecBwdPerSm, h.D, h.max_B, h.max_L);
+    const int group = h.dtype == FAVOR_DTYPE_F32 ? rec_group<float>() : rec_group<__nv_bfloat16>();
     const size_t slabs = (h.D + kRecSlab - 1) / kRecSlab;
-    const size_t tokens = (size_t)h.max_B * slabs * h.max_L + blocks * kRecWarps * (kRecRunMin + kRecGroupMax);
-    return blocks * 2 * (kRecWarps + 1) * kRecMapFloats + tokens / group * kRecMapFloats + blocks * 3 * kRecSlab;
+    return blocks * 2 * (kRecWarps + 1) * kRecMapFloats + blocks * 3 * kRecSlab +
+           (size_t)h.max_B * recur_groups(h.max_L, group) * slabs * kRecMapFloats;
 }
 
 favor_status recur_backward(const RecurHandle& h, const RecurArgs& a, cudaStream_t st) {

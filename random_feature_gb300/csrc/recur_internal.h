@@ -447,10 +447,13 @@ inline RecurPlan recur_plan(int num_sms, int per_sm, int D, int B, int L) {
     p.chunks = (int)((L + (long long)p.run * kRecWarps - 1) / ((long long)p.run * kRecWarps));
     return p;
 }
-// Chunks x slabs x rows of any call with at most these sizes: recur_plan's quotient, or a chunk a row.
-inline size_t recur_blocks_max(int num_sms, int per_sm, int D, int max_B) {
+// Chunks x slabs x rows of any call with at most these sizes: a chunk a row, or as many as recur_plan's quotient gives
+// and a row of max_L tokens fills.
+inline size_t recur_blocks_max(int num_sms, int per_sm, int D, int max_B, int max_L) {
     const size_t places = (size_t)num_sms * per_sm, columns = (size_t)max_B * ((D + kRecSlab - 1) / kRecSlab);
-    return places > columns ? places : columns;
+    const size_t filled = ((size_t)max_L + kRecWarps * kRecRunMin - 1) / (kRecWarps * kRecRunMin);
+    const size_t most = columns * (filled < kRecChunksMax ? filled : kRecChunksMax);
+    return columns > places ? columns : places < most ? places : most;
 }
 
 // f<T, RATE, SCALE>::go(args...) for the handle's storage and scale and the call's decay.
