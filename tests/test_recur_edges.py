@@ -86,7 +86,7 @@ def test_equal_decays_in_long_runs(rates, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("L", [1, 5, 300])
 def test_states_that_are_not_finite(L, dtype):
-    """An infinite or NaN state stays out of reach, in its own channel and row; rows without tokens leave theirs alone."""
+    """An infinite or NaN state stays in its own channel and row; rows without tokens leave theirs alone."""
     B, D = 3, 12
     s = inputs(B, L, D, dtype, 34)
     h0 = np.random.default_rng(35).standard_normal((B, D)).astype(np.float32)
