@@ -5,7 +5,7 @@
 //     dx = (dn - mean(dn) - n mean(dn n)) / sqrt(var + eps)   (no mean(dn) without centring),
 //     dweight = sum du n,  dbias = sum du over the tokens.
 // Nothing but bytes: every input is read once and every output written once, 25 instructions an element
-// forwards (28 by heads) and 43 back.  A group lies in the registers of the threads that share it: 1 to 32 lanes of a
+// forwards (28 by heads) and 46 back.  A group lies in the registers of the threads that share it: 1 to 32 lanes of a
 // warp (their sums by shuffles), or a whole block.  The mean comes before the squares of what is left,
 // so that an offset of the channels costs no digits.  A thread keeps its channels from token to token:
 // their parameters, and the sums of their gradients, stay in registers too, and the next token's
@@ -249,12 +249,15 @@ struct NormThread {
     }
 };
 
-// Threads of a block at most.
+// Threads of a block at most.  1024 leave a thread 64 registers, whatever the call's block has: the instances of 16
+// channels a thread (bf16 groups above 4096 channels, fp32 above 2048) spill, forwards 190 to 810 bytes a thread, back
+// 1000 to 1600 ([4, 4096, 5120] bf16 in one gated group 163 and 770 us, [4, 4096, 4096] 114 and 203).
 template <int V, int E, bool WIDE>
 __host__ __device__ constexpr int norm_threads() { return !WIDE ? 256 : V * E <= 8 ? 512 : 1024; }
 
 template <typename T, int V, int E, bool WIDE>
-__global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <= 8 ? 4 : 1) k_norm(NormArgs a, NormPlan p) {
+__global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <= 8 ? 4 : 1)
+k_norm(NormArgs a, NormPlan p) {
     __shared__ GroupSum sm;
     typedef NormThread<T, V, E, WIDE> Thread;
     constexpr int N = Thread::N;
@@ -304,7 +307,8 @@ __global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <
 }
 
 template <typename T, int V, int E, bool WIDE>
-__global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <= 8 ? 2 : 1) k_norm_bwd(NormArgs a, NormPlan p, float* part) {
+__global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <= 8 ? 2 : 1)
+k_norm_bwd(NormArgs a, NormPlan p, float* part) {
     __shared__ GroupSum sm;
     extern __shared__ float sums[];     // [E * V][threads]
     typedef NormThread<T, V, E, WIDE> Thread;
@@ -400,7 +404,8 @@ __global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <
             if (th.tb == 0)
                 for (int t = 1; t < p.tokens; ++t)
 #pragma unroll
-                    for (int i = 0; i < 2 * N; ++i) v[i] += sums[i * blockDim.x + threadIdx.x + t * p.per_block * p.share];
+                    for (int i = 0; i < 2 * N; ++i)
+                        v[i] += sums[i * blockDim.x + threadIdx.x + t * p.per_block * p.share];
         }
         if (th.tb == 0) {
 #pragma unroll
@@ -414,7 +419,8 @@ __global__ void __launch_bounds__((norm_threads<V, E, WIDE>()), !WIDE && V * E <
 }
 
 // part [rows][2][D] summed over rows in a fixed order: 32 columns a block, a warp every 32nd row, 8 of them at a time.
-__global__ void __launch_bounds__(1024) k_norm_reduce(const float* part, int rows, int D, float* dweight, float* dbias) {
+__global__ void __launch_bounds__(1024)
+k_norm_reduce(const float* part, int rows, int D, float* dweight, float* dbias) {
     __shared__ float s[32][33];
     const int n = 2 * D, lane = threadIdx.x & 31, y = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
     float sum = 0.f;
@@ -438,8 +444,10 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const float* part, int row
 }
 
 // ------------------------------------------------------------------ host
-// Blocks an SM at most: what fits at 64 registers (6 or 8 leave a part wave: by heads 88 and 78 us instead of 77), and for
-// gradients two waves of the two that fit (three at 80 registers spill: 137 us instead of 113; 6 waves 145).
+// Blocks an SM at most: what fits at 64 registers (6 or 8 leave a part wave: by heads 88 and 78 us instead of 77; the
+// narrow instances that read less than 16 bytes at a time, and fp32's of 8 channels a thread, spill 28 to 250 bytes
+// at it), and for gradients two waves of the two that fit (three at 80 registers spill: 137 us instead of 113; 6
+// waves 145).
 constexpr int kNormPerSm = 4, kNormBwdPerSm = 4;
 
 static NormPlan norm_plan(const NormHandle& h, int B, int L, int V, int E, bool wide, int per_sm) {

@@ -5,11 +5,12 @@
 // tokens, one a warp, as many as keep the device full.  k_recur_maps joins the maps of each run (x, r, i
 // are read); k_recur_scan takes each run's start from the maps in front of it and walks it again, now
 // writing the output.  No warp waits for another but at a block's start, and sums have one order.
-// 24 and 36 instructions an element, 12 of the slow kind (4 clocks of a quarter SM each) and some 44 packed or
-// single multiply-adds (1.45 clocks with three register operands); 16 elements moved for the 10 that are
-// the least.  [8, 4096, 1536] bf16: 156 us (3.2 TB/s of the 10; 5.2 of the 16), [1, 65536, 1024] 196 us; with no
-// arithmetic but the maps' 129 and 170.  In one
-// pass, with blocks of a cluster that hand the state on in step, these took 135 and 354 us (an exchange cost
+// 25 and 36 instructions an element, 12 of the slow kind (4 clocks of a quarter SM each) and some 45 packed or
+// single multiply-adds (1.45 clocks with three register operands); 8 elements are moved for the 5 that are
+// the least (x, r, i twice).  [8, 4096, 1536] bf16: 156 us (3.2 TB/s of the 5; 5.2 of the 8), [1, 65536, 1024] 196
+// us, and 129 and 170 when first measured with no arithmetic but the maps'.  That is where all rates of 128
+// neighbouring channels are below 0.125; the general form takes 192 and 239, that without rates 146 of the first.
+// In one pass, with blocks of a cluster that hand the state on in step, these took 135 and 354 us (an exchange cost
 // 0.7 us a step for two blocks, 1.4 for eight), and gradients 328 instead of 263; rows of a call in groups
 // of L2's size between the two kernels were no faster (46 us for a quarter of the first case).  The maps walk a run
 // from its end to its start, where the scan begins.
@@ -19,8 +20,8 @@
 
 namespace favor {
 
-// Blocks an SM: 16 warps of 128 registers.  Three blocks of 80 spill (209 us instead of 157), two channels a lane or two
-// tokens a group in their place 177; without the next group's rows on their way 169.
+// Blocks an SM: 16 warps of 128 registers.  Three blocks of 80 spill (209 us instead of 157), two channels a lane or
+// two tokens a group in their place 177; without the next group's rows on their way 169.
 constexpr int kRecPerSm = 2;
 
 // Grid: rows x chunks x slabs.
@@ -35,7 +36,8 @@ __global__ void __launch_bounds__(kRecThreads, kRecPerSm) k_recur_maps(RecurArgs
     const int len = row_len(a.lens, b, a.L);
     if (a.state && chunk == 0) {    // the state in front of the row, which the scan's last run will overwrite
         const int page = block_page(a.pg, b);
-        if (warp == 0 && page >= 0) first[((size_t)b * at.p.slabs + slab) * 32 + lane] = load_vec(a.state + (size_t)page * D, l);
+        if (warp == 0 && page >= 0)
+            first[((size_t)b * at.p.slabs + slab) * 32 + lane] = load_vec(a.state + (size_t)page * D, l);
     }
     const int t0 = (chunk * kRecWarps + warp) * at.p.run, end = min(len, t0 + at.p.run);
     F4 mh = {both(0.f), both(0.f)};     // the run's map: its decays' product, and its state from an empty start
@@ -100,8 +102,8 @@ __global__ void __launch_bounds__(kRecThreads, kRecPerSm) k_recur_maps(RecurArgs
 }
 
 template <typename T, bool RATE, int SCALE>
-__global__ void __launch_bounds__(kRecThreads, kRecPerSm) k_recur_scan(RecurArgs a, int D, RecurMapsAt at, const F4* first,
-                                                                       bool one_run) {
+__global__ void __launch_bounds__(kRecThreads, kRecPerSm)
+k_recur_scan(RecurArgs a, int D, RecurMapsAt at, const F4* first, bool one_run) {
     constexpr int G = rec_group<T>();
     __shared__ RecurPlaces places;
     const int slab = blockIdx.x % at.p.slabs, rest = blockIdx.x / at.p.slabs;

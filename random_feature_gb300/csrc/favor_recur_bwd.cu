@@ -8,15 +8,17 @@
 // the forward map from the run's start to every group of tokens; k_recur_bwd walks each run from its
 // end, with the state in front of each group from that map.  So five tensors are read twice and four
 // written: 14 elements for the 9 that are the least, and as much as 2 more for the groups' maps.
-// [4, 8192, 1024] bf16: 263 us (2.3 TB/s of the 9), 42 and 84 instructions an element; [2, 777, 500] fp32 20 us.
+// [4, 8192, 1024] bf16: 271 us (2.2 TB/s of the 9), 41 and 90 instructions an element (318 in the general form of
+// rates, 264 without rates); [2, 777, 500] fp32 20 us on the GPU (the call is the host's 37).
 #include <type_traits>
 
 #include "recur_internal.h"
 
 namespace favor {
 
-// Chunks for two blocks an SM, which the maps fill (128 registers); k_recur_bwd takes 246 registers, one block at a time
-// (capped at 128 it spills: 312 us; its rows through shared memory then 261; chunks for one block an SM 277).
+// Chunks for two blocks an SM, which the maps fill: 128 registers, and in bf16 12 to 100 bytes of spills.  k_recur_bwd
+// takes 255 in bf16, with up to 56 bytes of spills (239 at most and none in fp32), so one block at a time (capped at
+// 128 it took 312 us instead of 263; its rows through shared memory then 261; chunks for one block an SM 277).
 constexpr int kRecBwdPerSm = 2;
 
 // The maps from a run's start to its groups: [row][group of the row][slab] of a warp's lanes.
@@ -29,8 +31,8 @@ struct GroupMapsAt {
 };
 
 template <typename T, bool RATE, int SCALE>
-__global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(RecurArgs a, int D, RecurMapsAt fwd, RecurMapsAt rev,
-                                                                              GroupMapsAt groups) {
+__global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm)
+k_recur_bwd_maps(RecurArgs a, int D, RecurMapsAt fwd, RecurMapsAt rev, GroupMapsAt groups) {
     constexpr int G = rec_group<T>();
     __shared__ RecurMap runs[2][kRecWarps][32];
     const RecurPlan& p = fwd.p;
@@ -45,8 +47,8 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
     RunDecay ma, mb;
     if (t0 < end) {
         const size_t row0 = (size_t)b * a.L * D;
-        const T *x = (const T*)a.x + row0, *r = (const T*)a.r + row0, *gi = (const T*)a.i + row0, *z = (const T*)a.z + row0;
-        const T* dout = (const T*)a.dout + row0;
+        const T *x = (const T*)a.x + row0, *r = (const T*)a.r + row0, *gi = (const T*)a.i + row0;
+        const T *z = (const T*)a.z + row0, *dout = (const T*)a.dout + row0;
         const RecurChan4 par = load_chans<T>(a, l);
         auto group = [&](auto slow, auto whole, int t, auto vx, auto vr, auto vi, auto vz, auto vg) {
             constexpr bool SLOW = decltype(slow)::value;
@@ -138,8 +140,8 @@ __global__ void __launch_bounds__(kRecThreads, kRecBwdPerSm) k_recur_bwd_maps(Re
 
 // part [row and chunk][3][D]: each block's sums of drate, dr and di.
 template <typename T, bool RATE, int SCALE>
-__global__ void __launch_bounds__(kRecThreads, 1) k_recur_bwd(RecurArgs a, int D, RecurMapsAt fwd, RecurMapsAt rev,
-                                                                         GroupMapsAt groups, float* part) {
+__global__ void __launch_bounds__(kRecThreads, 1)
+k_recur_bwd(RecurArgs a, int D, RecurMapsAt fwd, RecurMapsAt rev, GroupMapsAt groups, float* part) {
     constexpr int G = rec_group<T>();
     __shared__ RecurPlaces places;
     __shared__ F4 sums[kRecWarps][3][32];
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kRecThreads, 1) k_recur_bwd(RecurArgs a, int D
             const F4 h0 = apply(*groups(p, b, t / G, slab), start);
             typedef typename Raw4<T>::H H;
             H ox[2][G], orr[2][G], oi[2][G], oz[2][G];
-            // one pair of channels after the other: both at once take more registers than two blocks an SM leave
+            // one pair of channels after the other: even so this takes all the registers that a thread can have
             auto half = [&](int k, F2 h, const RecurChan& c, F2& m, F2& srate, F2& sr, F2& ss) {
                 F2 hs[G + 1];       // the states in front of the group's tokens, and behind it
                 hs[0] = h;

@@ -41,7 +41,8 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 template <typename T>
 __device__ __forceinline__ F2 sigmoid_bias(F2 b) { return sizeof(T) == 2 ? b * both(-kLog2e) : b; }
 // sigmoid(x + bias).  16-bit storage: one product and one sum make the exponent, and the approximate forms follow;
-// the relative error is under 2^-20 for |x|, |bias| < 16.  fp32: sigmoids.
+// the relative error is under 2^-18 for |x|, |bias| < 16 (two roundings of an exponent of up to 46, 3 2^-20 in it).
+// fp32: sigmoids.
 template <typename T>
 __device__ __forceinline__ F2 sigmoid2(F2 x, F2 bias) {
     if (sizeof(T) == 2) {
@@ -50,9 +51,10 @@ __device__ __forceinline__ F2 sigmoid2(F2 x, F2 bias) {
     }
     return each(x + bias, [](float v) { float s, n; sigmoids<T>(v, s, n); return s; });
 }
-// sigmoid(x) and sigmoid(-x) = e sigmoid(x), e = e^-x, which is kept finite for it (but a NaN, a NaN).  sigmoid(x) itself
-// is 0 from there on, as a product with an x of the type's lowest value has to be (2^-126 makes -4 of bf16's).  KEPT:
-// 2^-126 stays, for a decay, whose state is nowhere near 2^126 (the recurrence without rates is 3% slower with the 0).
+// sigmoid(x) and sigmoid(-x) = e sigmoid(x), e = e^-x, which is kept finite for it (but a NaN, a NaN).  sigmoid(x)
+// itself is 0 from there on, as a product with an x of the type's lowest value has to be (2^-126 makes -4 of bf16's).
+// KEPT: 2^-126 stays, for a decay, whose state is nowhere near 2^126 (the recurrence without rates takes 3% longer
+// with the 0).
 template <typename T, bool KEPT = false>
 __device__ __forceinline__ void sigmoids2(F2 x, F2 bias, F2& s, F2& sn) {
     if (sizeof(T) == 2) {
@@ -80,7 +82,9 @@ __device__ __forceinline__ F2 silu2(F2 x) {
     return x * sigmoid2<T>(x, both(0.f));
 }
 
-__device__ __forceinline__ F2 to_f2(uint32_t u) { return F2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+__device__ __forceinline__ F2 to_f2(uint32_t u) {
+    return F2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t from_f2(F2 x, __nv_bfloat16) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(x.x(), x.y());
     return *reinterpret_cast<const uint32_t*>(&a);

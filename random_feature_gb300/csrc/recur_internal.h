@@ -186,11 +186,13 @@ __device__ __forceinline__ F2 to_f2(float4 u, int half) { return half ? F2(u.z, 
 __device__ __forceinline__ uint2 raw_of(uint32_t a, uint32_t b) { return make_uint2(a, b); }
 __device__ __forceinline__ float4 raw_of(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
 template <typename T>
-__device__ __forceinline__ typename Raw4<T>::V from_f4(const F4& x) { return raw_of(from_f2(x.a, T()), from_f2(x.b, T())); }
-// What a lane needs to walk rows: its four channels, which are neighbours where rows are moved 4 channels at a time, else
-// two pairs 64 channels apart, or 32 channels apart one by one, so that a warp's accesses stay whole; those
-// that are not there (at D and behind) count for nothing.  [4, 4096, 1001] bf16 119 us (neighbours read one by one, each
-// in a branch of its own, 256), gradients 345 (642); [4, 4096, 1000] 62 and 151.
+__device__ __forceinline__ typename Raw4<T>::V from_f4(const F4& x) {
+    return raw_of(from_f2(x.a, T()), from_f2(x.b, T()));
+}
+// What a lane needs to walk rows: its four channels, which are neighbours where rows are moved 4 channels at a time,
+// else two pairs 64 channels apart, or 32 channels apart one by one, so that a warp's accesses stay whole; those
+// that are not there (at D and behind) count for nothing.  [4, 4096, 1001] bf16 123 us (neighbours read one by one,
+// each in a branch of its own, 256 at the time), gradients 335 (642); [4, 4096, 1024] 62 and 154.
 struct RecurLane {
     int D, width, c;    // c: the first channel
     bool quads;
@@ -211,7 +213,8 @@ struct RecurLane {
 // together: for a channel that is not there the row's last one is read.
 __device__ __forceinline__ uint2 raw_part(const __nv_bfloat16* p, const RecurLane& l) {
     if (l.width == 2)
-        return make_uint2(*reinterpret_cast<const uint32_t*>(p + l.last(0, 2)), *reinterpret_cast<const uint32_t*>(p + l.last(2, 2)));
+        return make_uint2(*reinterpret_cast<const uint32_t*>(p + l.last(0, 2)),
+                          *reinterpret_cast<const uint32_t*>(p + l.last(2, 2)));
     const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
     const uint32_t a = q[l.last(0, 1)], b = q[l.last(1, 1)], c = q[l.last(2, 1)], d = q[l.last(3, 1)];
     return make_uint2(a | b << 16, c | d << 16);
@@ -300,7 +303,8 @@ __device__ __forceinline__ RecurChan4 load_chans(const RecurArgs& a, const Recur
     p.a = {rate.a, sigmoid_bias<T>(rb.a), sigmoid_bias<T>(ib.a), false};
     p.b = {rate.b, sigmoid_bias<T>(rb.b), sigmoid_bias<T>(ib.b), false};
     auto slow = [](float v) { return v >= 0.f && v < kSlowRate; };
-    p.a.slow = p.b.slow = a.rate && __all_sync(~0u, slow(rate.a.x()) && slow(rate.a.y()) && slow(rate.b.x()) && slow(rate.b.y()));
+    const bool mine = slow(rate.a.x()) && slow(rate.a.y()) && slow(rate.b.x()) && slow(rate.b.y());
+    p.a.slow = p.b.slow = a.rate && __all_sync(~0u, mine);
     return p;
 }
 
@@ -350,7 +354,9 @@ struct alignas(16) RecurMap {
 __device__ __forceinline__ RecurMap no_map() {
     return {{both(1.f), both(1.f)}, {both(0.f), both(0.f)}};
 }
-__device__ __forceinline__ F4 apply(const RecurMap& m, const F4& x) { return {fma2(m.p.a, x.a, m.h.a), fma2(m.p.b, x.b, m.h.b)}; }
+__device__ __forceinline__ F4 apply(const RecurMap& m, const F4& x) {
+    return {fma2(m.p.a, x.a, m.h.a), fma2(m.p.b, x.b, m.h.b)};
+}
 // first, then `then`.
 __device__ __forceinline__ RecurMap join(const RecurMap& first, const RecurMap& then) {
     return {{first.p.a * then.p.a, first.p.b * then.p.b}, apply(then, first.h)};
@@ -394,7 +400,8 @@ struct RunDecay {
     }
 };
 
-// The maps of a call's runs and chunks, in the workspace: [row][chunk][run][slab] and [row][chunk][slab] of a warp's lanes.
+// The maps of a call's runs and chunks, in the workspace: [row][chunk][run][slab] and [row][chunk][slab] of a warp's
+// lanes.
 struct RecurMapsAt {
     RecurMap *run, *chunk;
     RecurPlan p;
@@ -406,7 +413,9 @@ struct RecurMapsAt {
     }
 };
 constexpr size_t kRecMapFloats = 32 * (sizeof(RecurMap) / 4);     // of a warp's lanes
-inline size_t recur_run_floats(const RecurPlan& p, int B) { return (size_t)B * p.chunks * kRecWarps * p.slabs * kRecMapFloats; }
+inline size_t recur_run_floats(const RecurPlan& p, int B) {
+    return (size_t)B * p.chunks * kRecWarps * p.slabs * kRecMapFloats;
+}
 inline size_t recur_chunk_floats(const RecurPlan& p, int B) { return (size_t)B * p.chunks * p.slabs * kRecMapFloats; }
 
 // For every warp of a block: the state in front of the warp's run, from `start` in front of the row.  REVERSE:
@@ -433,8 +442,10 @@ __device__ __forceinline__ F4 run_start(const RecurMapsAt& at, int b, int chunk,
     return start;
 }
 
-// Runs of 8 tokens at least: [3, 1000, 500] fp32 13.9 us, 17.4 with 16.  Chunks of a row: as many blocks as the device holds at once (`per_sm` an SM), but kRecChunksMax at most (see
-// run_start) and no run under kRecRunMin tokens.
+// Chunks of a row: as many blocks as the device holds at once (`per_sm` an SM), but kRecChunksMax at most (see
+// run_start) and no run under kRecRunMin tokens: 8, with which [3, 1000, 500] fp32 took 13.9 us on the GPU, and 17.4
+// with 16 (the call is the host's 19).  One wave of blocks and no more: where B * slabs comes to just over half of it,
+// or just over all of it, the rest stands idle ([8, 4096, 2048] 220 us, [8, 4096, 2560] 412, [8, 4096, 5120] 652).
 inline RecurPlan recur_plan(int num_sms, int per_sm, int D, int B, int L) {
     RecurPlan p;
     p.slabs = (D + kRecSlab - 1) / kRecSlab;

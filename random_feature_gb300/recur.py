@@ -202,7 +202,8 @@ class Recurrence(_Owner):
         out = self._new(x, shape, stream, out)
         _check(self._lib.favor_recur_scan(self.handle, x.data_ptr(), r.data_ptr(), _at(i), _at(rate), _at(r_bias),
                                           _at(i_bias), _at(z), _at(state), _at(pages), P, _at(lens), clear,
-                                          out.data_ptr(), shape[0], shape[1], _raw_stream(stream, self._index)), "favor_recur_scan")
+                                          out.data_ptr(), shape[0], shape[1], _raw_stream(stream, self._index)),
+               "favor_recur_scan")
         return out
 
     def step(self, x, r, state, i=None, rate=None, r_bias=None, i_bias=None, z=None, pages=None, out=None,
@@ -257,7 +258,8 @@ class GroupNorm(_Owner):
             raise ValueError(f"x: expected 2, 3 or 4 dimensions, got {list(x.shape)}")
         rows, vec = ((B,), self._i32, self.device), self._vec
         like_x, like_out = (kind, self._t, self.device), (shape, self._t, self.device)
-        if not (_fits(x, like_x) and _fits(z, like_out) and _fits(weight, vec) and _fits(bias, vec) and _fits(lens, rows)):
+        if not (_fits(x, like_x) and _fits(z, like_out) and _fits(weight, vec) and _fits(bias, vec)
+                and _fits(lens, rows)):
             self._check_all(((x, like_x, "x"), (z, like_out, "z"), (weight, vec, "weight"), (bias, vec, "bias"),
                              (lens, rows, "lens")))
         return shape, 1 if dims == 4 else 0, B, L
@@ -268,7 +270,8 @@ class GroupNorm(_Owner):
         clear = 1 if out is None else 0
         out = self._new(x, shape, stream, out)
         _check(self._lib.favor_group_norm(self.handle, x.data_ptr(), heads, _at(weight), _at(bias), _at(z), _at(lens),
-                                          clear, out.data_ptr(), B, L, _raw_stream(stream, self._index)), "favor_group_norm")
+                                          clear, out.data_ptr(), B, L, _raw_stream(stream, self._index)),
+               "favor_group_norm")
         return out
 
     def backward(self, x, dout, weight=None, bias=None, z=None, lens=None, stream=None):
