@@ -1,4 +1,6 @@
 """GPU test of what a handle of the gated linear recurrence allocates, against what the header states."""
+import gc
+
 import pytest
 import torch
 
@@ -28,6 +30,7 @@ def test_workspace(D, dtype, max_B, max_L, training):
     """Free memory moves in blocks of 2 MB; what a process allocates in its first calls comes before."""
     with R.Recurrence(D, dtype, 1, 9) as f:
         f.new_state(1)
+    gc.collect()        # handles of other tests
     torch.cuda.synchronize()
     before = torch.cuda.mem_get_info()[0]
     with R.Recurrence(D, dtype, max_B, max_L, training=training):
